@@ -499,6 +499,143 @@ MOE_API int moe_permute_static(const moe_shape_t *shape, const int32_t *topk_idx
                                int32_t *slot_pos, int32_t *perm_token, moe_bf16_t *x_perm,
                                int32_t *n_kept, uint32_t *status, moe_stream_t stream);
 
+/* ---- Linear products with bias, activation and residual, dense or grouped by
+ * expert with ragged sizes: the experts and neighbouring layers that are not
+ * the packed SwiGLU pair ("Expert FFN" with another activation or with biases;
+ * the plain FFN blocks of "Switch Transformers" and the GLaM row). For group e
+ * and every row r of its segment [offsets[e], offsets[e+1]):
+ *   z[r] = x[r] W_e^T + b_e          y[r] = act(z[r]) + residual[r]
+ * x, W, z, y, residual and the gradients of x and W are bf16, biases and
+ * their gradients fp32; every product is accumulated in fp32 and y is rounded
+ * once, from the unrounded z. */
+
+/* Activations (moe_linear_t.act). */
+enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,      /* max(z, 0); derivative 0 at z <= 0 */
+    MOE_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+    MOE_ACT_GELU_TANH = 3, /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    MOE_ACT_SILU = 4       /* z / (1 + e^-z) */
+};
+
+/* Shape of a linear product. Requirements (else MOE_ERR_INVALID_ARG):
+ *   0 <= rows <= 2^24; d_in and d_out multiples of 8 in [8, 65536];
+ *   1 <= E <= MOE_MAX_E; act one of MOE_ACT_*; flags 0.
+ * Groups: expert_offsets [E+1] int32 on the device (as moe_permute writes
+ * them), 0 <= offsets[0] <= ... <= offsets[E] <= rows; groups may be empty,
+ * and rows outside every group are neither read into a result nor written.
+ * expert_offsets = NULL is the dense product: E = 1 and all rows. Offsets that
+ * break the rule set MOE_ERR_CHECK in *status, and the call treats every
+ * group as empty. */
+typedef struct moe_linear {
+    int32_t rows, d_in, d_out;
+    int32_t E;
+    int32_t act;
+    int32_t flags;
+} moe_linear_t;
+
+/* Bytes of workspace that moe_linear_backward needs for this shape. */
+MOE_API int moe_linear_workspace_size(const moe_linear_t *shape, size_t *bytes);
+
+/* y = act(x W^T + b) + residual.
+ *   x [rows, d_in] bf16; W [E, d_out, d_in] bf16 (nn.Linear [out, in]);
+ *   bias [E, d_out] fp32 or NULL; residual [rows, d_out] bf16 or NULL;
+ *   y [rows, d_out] bf16 out (may be the residual itself: each element is read
+ *   before it is written, by the same thread; no other overlap is allowed);
+ *   z [rows, d_out] bf16 out or NULL: the pre-activation, for the backward.
+ * The same inputs give the same bits on every call. Device errors:
+ * MOE_ERR_CHECK (offsets), MOE_ERR_TIMEOUT. */
+MOE_API int moe_linear_forward(const moe_linear_t *shape, const moe_bf16_t *x,
+                               const int32_t *expert_offsets, const moe_bf16_t *W,
+                               const float *bias, const moe_bf16_t *residual, moe_bf16_t *y,
+                               moe_bf16_t *z, uint32_t *status, moe_stream_t stream);
+
+/* Gradients of sum(y * dy) with the same x, W, expert_offsets:
+ *   dz = dy act'(z); dx = dz W_e; dW_e = sum_r dz[r]^T x[r]; dbias_e = sum_r dz[r]
+ * (the residual's gradient is dy itself).
+ *   z  [rows, d_out] bf16 as moe_linear_forward wrote it (NULL with
+ *      MOE_ACT_NONE, else required); dy [rows, d_out] bf16
+ *   dx [rows, d_in] bf16 out or NULL; rows outside every group untouched
+ *   dW [E, d_out, d_in] bf16 out or NULL; dbias [E, d_out] fp32 out or NULL:
+ *      fully written (zero for an empty group, and for rows = 0)
+ * Outputs overlap no input. W may be NULL when dx is, x when dW is. With an
+ * activation dz is rounded to bf16 for the products (dbias sums it
+ * unrounded). The same inputs give the same bits on every call. Calls that
+ * share a workspace must be ordered on the GPU, replays of captured graphs
+ * among them. Device errors: MOE_ERR_CHECK (offsets), MOE_ERR_TIMEOUT. */
+MOE_API int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
+                                const int32_t *expert_offsets, const moe_bf16_t *W,
+                                const moe_bf16_t *z, const moe_bf16_t *dy, moe_bf16_t *dx,
+                                moe_bf16_t *dW, float *dbias, uint32_t *status, void *ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* ---- Combine of bf16 expert rows and its gradient ("Sparse MoE Block": scale by
+ * the routing weight, index_add into token order), for expert rows that
+ * moe_linear_forward wrote. Only T, d and k of the shape are used (its rules
+ * apply to all fields).
+ * moe_combine_rows:
+ *   out[t] = residual[t] + sum_{j, slot_pos[t,j] >= 0} w[t,j] y_perm[slot_pos[t,j]]
+ *   y_perm [T*k, d] bf16; slot_pos [T, k] int32 (moe_permute; negative: dropped);
+ *   topk_w [T, k] fp32 or NULL (all weights 1: with y_perm the gradient of the
+ *   permuted rows, this is the gradient of moe_permute's gather);
+ *   residual [T, d] bf16 or NULL (may be out); out [T, d] bf16. Summed in fp32
+ *   in slot order and rounded once.
+ * moe_combine_rows_backward, of sum(out * dout):
+ *   dy_perm[slot_pos[t,j]] = w[t,j] dout[t]     (bf16; other rows untouched)
+ *   dtopk_w[t,j] = <dout[t], y_perm[slot_pos[t,j]]>, 0 for a dropped slot
+ *   y_perm may be NULL when dtopk_w is; dy_perm or dtopk_w may be NULL. Each row
+ *   of dy_perm is the slot of at most one (t, j).
+ * A slot_pos >= T*k is treated as dropped and sets MOE_ERR_CHECK in *status. */
+MOE_API int moe_combine_rows(const moe_shape_t *shape, const moe_bf16_t *y_perm,
+                             const int32_t *slot_pos, const float *topk_w,
+                             const moe_bf16_t *residual, moe_bf16_t *out, uint32_t *status,
+                             moe_stream_t stream);
+MOE_API int moe_combine_rows_backward(const moe_shape_t *shape, const moe_bf16_t *dout,
+                                      const moe_bf16_t *y_perm, const int32_t *slot_pos,
+                                      const float *topk_w, moe_bf16_t *dy_perm, float *dtopk_w,
+                                      uint32_t *status, moe_stream_t stream);
+
+/* ---- Global gradient norm over many tensors, and clipping (for the gradients
+ * of moe_backward and moe_linear_backward together). Types of one tensor: */
+enum {
+    MOE_TYPE_F32 = 0,
+    MOE_TYPE_BF16 = 1
+};
+
+/* Workspace of the two calls below, for any tensors. */
+#define MOE_GRAD_WS_BYTES 65536
+
+/* norm[0] = sqrt(sum over all tensors of sum g^2), fp32, on the device.
+ *   n       number of tensors, 0 <= n <= 2^20 (norm = 0 for none)
+ *   grads   HOST array of n device pointers; numel HOST array of n int64
+ *           element counts (0 <= numel <= 2^40; a pointer may be NULL where it is
+ *           0); types HOST array of n MOE_TYPE_*. The arrays are read before the
+ *           call returns. Tensors are contiguous and aligned to their element
+ *           size (16 bytes is faster).
+ * Squares are summed in fp32 over runs of at most 32 elements and in fp64
+ * beyond; a run whose fp32 sum leaves the normal range is summed in fp64, so
+ * the norm is finite whenever it fits fp32. The order of the sums is fixed: the
+ * same call gives the same bits. A norm that is infinite or NaN sets
+ * MOE_ERR_NONFINITE in *status. */
+MOE_API int moe_grad_norm(int n, const void *const *grads, const int64_t *numel,
+                          const int32_t *types, float *norm, uint32_t *status, void *ws,
+                          size_t ws_bytes, moe_stream_t stream);
+
+/* The norm as above, then every gradient scaled by
+ *   c = min(1, max_norm / (norm + 1e-6))
+ *   outs   HOST array of n device pointers of the same types, or NULL: in
+ *          place. outs[i] may be grads[i]; no other overlap between any two of
+ *          the tensors.
+ * In place, a factor of 1 writes nothing. A norm that is infinite or NaN sets
+ * MOE_ERR_NONFINITE; the gradients are then left as they are (out of place:
+ * copied), so that the caller can skip the step. max_norm must be > 0 and not
+ * NaN; tensors that overlap, within grads or within outs or between them
+ * otherwise than outs[i] = grads[i], are refused (MOE_ERR_INVALID_ARG). */
+MOE_API int moe_clip_grads(int n, const void *const *grads, void *const *outs,
+                           const int64_t *numel, const int32_t *types, float max_norm,
+                           float *norm, uint32_t *status, void *ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
 /* ---- Instrumentation (computes nothing; for measurement and tests). ---- */
 
 /* Stages of moe_forward (and moe_backward) timed by the profiler below; in

@@ -8,6 +8,7 @@ library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -43,6 +44,16 @@ MOE_FLAG_NVFP4 = 1 << 11
 MOE_FLAG_DEBUG_CHECKS = 1 << 12
 MOE_FLAG_TEST_TIMEOUT = 1 << 13
 
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_GELU_TANH = 3
+MOE_ACT_SILU = 4
+
+MOE_TYPE_F32 = 0
+MOE_TYPE_BF16 = 1
+MOE_GRAD_WS_BYTES = 65536
+
 MOE_MAX_E = 256
 MOE_MAX_K = 16
 MOE_DECODE_MAX_T = 16
@@ -63,8 +74,20 @@ class moe_shape_t(ctypes.Structure):
         return "moe_shape_t(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
+class moe_linear_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("act", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+    def __repr__(self):
+        return "moe_linear_t(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
 def make_shape(T, d, d_ff, E, k, capacity=0, d_ff_shared=0, flags=0) -> moe_shape_t:
     return moe_shape_t(T, d, d_ff, E, k, capacity, d_ff_shared, flags)
+
+
+def make_linear(rows, d_in, d_out, E=1, act=MOE_ACT_NONE, flags=0) -> moe_linear_t:
+    return moe_linear_t(rows, d_in, d_out, E, act, flags)
 
 
 def shape_of(workload, flags=0, T=None) -> moe_shape_t:
@@ -77,6 +100,7 @@ _lib = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _SHP = ctypes.POINTER(moe_shape_t)
+_LIN = ctypes.POINTER(moe_linear_t)
 
 _SIGS = {
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -100,6 +124,13 @@ _SIGS = {
     "moe_route_expert_choice": ([_SHP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "moe_forward_expert_choice": ([_SHP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
                                   ctypes.c_int),
+    "moe_linear_workspace_size": ([_LIN, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "moe_linear_forward": ([_LIN] + [_P] * 9, ctypes.c_int),
+    "moe_linear_backward": ([_LIN] + [_P] * 10 + [_SZ, _P], ctypes.c_int),
+    "moe_combine_rows": ([_SHP] + [_P] * 7, ctypes.c_int),
+    "moe_combine_rows_backward": ([_SHP] + [_P] * 8, ctypes.c_int),
+    "moe_grad_norm": ([ctypes.c_int] + [_P] * 6 + [_SZ, _P], ctypes.c_int),
+    "moe_clip_grads": ([ctypes.c_int] + [_P] * 4 + [ctypes.c_float] + [_P] * 3 + [_SZ, _P], ctypes.c_int),
     "moe_kernel_launches": ([], ctypes.c_uint64),
     "moe_profile_enable": ([ctypes.c_int], ctypes.c_int),
     "moe_profile_read": ([_P, _P, ctypes.c_int], ctypes.c_int),
@@ -152,6 +183,10 @@ def _ptr(t, dtype=None, name="tensor"):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _nbytes(ws):
+    return ws.numel() * ws.element_size() if ws is not None else 0
 
 
 def _host_ptr(t, dtype, name):
@@ -352,6 +387,170 @@ def moe_forward_host(shape, x_host, Wg, bias, W13, W2, W13_shared, W2_shared, ou
         _ptr(W13_shared, BF16, "W13_shared"), _ptr(W2_shared, BF16, "W2_shared"),
         _host_ptr(out_host, F32, "out_host"), _ptr(status, U32, "status"), _ptr(ws, name="ws"),
         ws.numel(), _stream(stream)))
+
+
+def _on_one_device(**tensors):
+    """Context in which the tensors' device is the current one (the library launches on
+    the current device); raises ValueError when they live on more than one."""
+    devs = {t.device for t in tensors.values() if isinstance(t, torch.Tensor) and t.is_cuda}
+    if len(devs) > 1:
+        raise ValueError("tensors on different devices: " + ", ".join(
+            f"{n} on {t.device}" for n, t in tensors.items()
+            if isinstance(t, torch.Tensor) and t.is_cuda))
+    return torch.cuda.device(devs.pop()) if devs else contextlib.nullcontext()
+
+
+def _has(t, shape, name):
+    if t is not None and isinstance(t, torch.Tensor) and tuple(t.shape) not in (
+            tuple(shape), tuple(shape[1:]) if shape[0] == 1 else tuple(shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _at_least(t, n, name):
+    if t is not None and isinstance(t, torch.Tensor) and t.numel() < n:
+        raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+
+
+def moe_linear_workspace_size(shape: moe_linear_t) -> int:
+    n = _SZ(0)
+    _check("moe_linear_workspace_size",
+           lib().moe_linear_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_linear_workspace(shape: moe_linear_t, device="cuda") -> torch.Tensor:
+    """A workspace for moe_linear_backward (torch allocates; the library never does)."""
+    return torch.empty(moe_linear_workspace_size(shape), dtype=torch.uint8, device=device)
+
+
+def moe_linear_forward(shape, x, expert_offsets, W, bias, residual, y, z=None, status=None,
+                       stream=None):
+    """y = act(x W_e^T + b_e) + residual over the groups of expert_offsets (None: dense, E = 1);
+    z (optional) receives the pre-activation. With E = 1, W and bias may lack the expert axis."""
+    R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
+    for t, shp, name in ((x, (R, di), "x"), (W, (E, do, di), "W"), (bias, (E, do), "bias"),
+                         (residual, (R, do), "residual"), (y, (R, do), "y"), (z, (R, do), "z")):
+        _has(t, shp, name)
+    _at_least(expert_offsets, E + 1, "expert_offsets")
+    _at_least(status, 1, "status")
+    with _on_one_device(x=x, expert_offsets=expert_offsets, W=W, bias=bias, residual=residual, y=y,
+                        z=z, status=status):
+        _check("moe_linear_forward", lib().moe_linear_forward(
+            ctypes.byref(shape), _ptr(x, BF16, "x"), _ptr(expert_offsets, I32, "expert_offsets"),
+            _ptr(W, BF16, "W"), _ptr(bias, F32, "bias"), _ptr(residual, BF16, "residual"),
+            _ptr(y, BF16, "y"), _ptr(z, BF16, "z"), _ptr(status, U32, "status"), _stream(stream)))
+    return y
+
+
+def moe_linear_backward(shape, x, expert_offsets, W, z, dy, dx, dW, dbias, status, ws, stream=None):
+    """Gradients of sum(y * dy): dx, dW and dbias (each may be None)."""
+    R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
+    for t, shp, name in ((x, (R, di), "x"), (W, (E, do, di), "W"), (z, (R, do), "z"),
+                         (dy, (R, do), "dy"), (dx, (R, di), "dx"), (dW, (E, do, di), "dW"),
+                         (dbias, (E, do), "dbias")):
+        _has(t, shp, name)
+    _at_least(expert_offsets, E + 1, "expert_offsets")
+    _at_least(status, 1, "status")
+    with _on_one_device(x=x, expert_offsets=expert_offsets, W=W, z=z, dy=dy, dx=dx, dW=dW,
+                        dbias=dbias, status=status, ws=ws):
+        _check("moe_linear_backward", lib().moe_linear_backward(
+            ctypes.byref(shape), _ptr(x, BF16, "x"), _ptr(expert_offsets, I32, "expert_offsets"),
+            _ptr(W, BF16, "W"), _ptr(z, BF16, "z"), _ptr(dy, BF16, "dy"), _ptr(dx, BF16, "dx"),
+            _ptr(dW, BF16, "dW"), _ptr(dbias, F32, "dbias"), _ptr(status, U32, "status"),
+            _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+
+
+def moe_combine_rows(shape, y_perm, slot_pos, topk_w, residual, out, status=None, stream=None):
+    """out[t] = residual[t] + sum_j w[t,j] y_perm[slot_pos[t,j]], bf16 rows (topk_w None: all 1)."""
+    T, d, k = shape.T, shape.d, shape.k
+    for t, shp, name in ((y_perm, (T * k, d), "y_perm"), (slot_pos, (T, k), "slot_pos"),
+                         (topk_w, (T, k), "topk_w"), (residual, (T, d), "residual"),
+                         (out, (T, d), "out")):
+        _has(t, shp, name)
+    _at_least(status, 1, "status")
+    with _on_one_device(y_perm=y_perm, slot_pos=slot_pos, topk_w=topk_w, residual=residual, out=out,
+                        status=status):
+        _check("moe_combine_rows", lib().moe_combine_rows(
+            ctypes.byref(shape), _ptr(y_perm, BF16, "y_perm"), _ptr(slot_pos, I32, "slot_pos"),
+            _ptr(topk_w, F32, "topk_w"), _ptr(residual, BF16, "residual"), _ptr(out, BF16, "out"),
+            _ptr(status, U32, "status"), _stream(stream)))
+    return out
+
+
+def moe_combine_rows_backward(shape, dout, y_perm, slot_pos, topk_w, dy_perm, dtopk_w, status=None,
+                              stream=None):
+    """Gradients of sum(out * dout) of moe_combine_rows: dy_perm and dtopk_w (either may be None)."""
+    T, d, k = shape.T, shape.d, shape.k
+    for t, shp, name in ((dout, (T, d), "dout"), (y_perm, (T * k, d), "y_perm"),
+                         (slot_pos, (T, k), "slot_pos"), (topk_w, (T, k), "topk_w"),
+                         (dy_perm, (T * k, d), "dy_perm"), (dtopk_w, (T, k), "dtopk_w")):
+        _has(t, shp, name)
+    _at_least(status, 1, "status")
+    with _on_one_device(dout=dout, y_perm=y_perm, slot_pos=slot_pos, topk_w=topk_w, dy_perm=dy_perm,
+                        dtopk_w=dtopk_w, status=status):
+        _check("moe_combine_rows_backward", lib().moe_combine_rows_backward(
+            ctypes.byref(shape), _ptr(dout, BF16, "dout"), _ptr(y_perm, BF16, "y_perm"),
+            _ptr(slot_pos, I32, "slot_pos"), _ptr(topk_w, F32, "topk_w"),
+            _ptr(dy_perm, BF16, "dy_perm"), _ptr(dtopk_w, F32, "dtopk_w"),
+            _ptr(status, U32, "status"), _stream(stream)))
+
+
+def _tensor_list(tensors, name):
+    """(pointers, element counts, MOE_TYPE_*) of fp32 / bf16 tensors, as host arrays."""
+    kinds = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
+    n = len(tensors)
+    ptrs, numel, types = (_P * max(n, 1))(), (ctypes.c_int64 * max(n, 1))(), (ctypes.c_int32 * max(n, 1))()
+    for i, t in enumerate(tensors):
+        p = _ptr(t, None, f"{name}[{i}]")
+        if t.dtype not in kinds:
+            raise TypeError(f"{name}[{i}]: expected float32 or bfloat16, got {t.dtype}")
+        ptrs[i], numel[i], types[i] = p, t.numel(), kinds[t.dtype]
+    return ptrs, numel, types
+
+
+def alloc_grad_workspace(grads=(), device="cuda") -> torch.Tensor:
+    """A workspace for moe_grad_norm and moe_clip_grads, on the gradients' device."""
+    dev = grads[0].device if len(grads) else device
+    return torch.empty(MOE_GRAD_WS_BYTES, dtype=torch.uint8, device=dev)
+
+
+def moe_grad_norm(grads, norm, status=None, ws=None, stream=None):
+    """norm[0] = the global 2-norm of a list of fp32 / bf16 tensors."""
+    grads = list(grads)
+    ptrs, numel, types = _tensor_list(grads, "grads")
+    _at_least(norm, 1, "norm")
+    _at_least(status, 1, "status")
+    with _on_one_device(norm=norm, status=status, ws=ws,
+                        **{f"grads[{i}]": t for i, t in enumerate(grads)}):
+        _check("moe_grad_norm", lib().moe_grad_norm(
+            len(grads), ptrs, numel, types, _ptr(norm, F32, "norm"), _ptr(status, U32, "status"),
+            _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+    return norm
+
+
+def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, stream=None):
+    """norm[0] = the global 2-norm, and every gradient scaled by min(1, max_norm / (norm + 1e-6)):
+    in place, or into `outs`."""
+    grads = list(grads)
+    ptrs, numel, types = _tensor_list(grads, "grads")
+    optrs = None
+    named = {f"grads[{i}]": t for i, t in enumerate(grads)}
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != len(grads):
+            raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.dtype != o.dtype or g.numel() != o.numel():
+                raise ValueError(f"outs[{i}]: must match grads[{i}] in type and size")
+        optrs, _, _ = _tensor_list(outs, "outs")
+        named |= {f"outs[{i}]": t for i, t in enumerate(outs)}
+    _at_least(norm, 1, "norm")
+    _at_least(status, 1, "status")
+    with _on_one_device(norm=norm, status=status, ws=ws, **named):
+        _check("moe_clip_grads", lib().moe_clip_grads(
+            len(grads), ptrs, optrs, numel, types, float(max_norm), _ptr(norm, F32, "norm"),
+            _ptr(status, U32, "status"), _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+    return norm
 
 
 # ---------------------------------------------------------------- convenience
