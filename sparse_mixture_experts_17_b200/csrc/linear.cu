@@ -5,8 +5,8 @@
 // ("Expert FFN" and "Sparse MoE Block" on "MoE Model Architectures" with another
 // activation, with biases, or alone.)
 //
-// This file holds the entry points, the elementwise pass of the backward and
-// the product kernels.
+// This file holds the entry points and the elementwise pass of the backward;
+// the products are in linear_tc.cu.
 #include <algorithm>
 #include <cstring>
 
@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "groups.cuh"
 #include "internal.h"
+#include "linear.h"
 
 namespace moe {
 
@@ -108,122 +109,6 @@ __global__ void __launch_bounds__(256)
     db[(long long)e * d_out + c] = s;
 }
 
-// ---------------------------------------------------------------- products (CUDA cores)
-// out[c, m] = sum_k A[m, k] B[c, k], 64 x 64 tiles. LIN_FWD: m = d_out, c = rows,
-// k = d_in. LIN_DX: m = d_in, c = rows, k = d_out. LIN_DW: m = d_in, c = d_out,
-// k = the group's rows.
-enum LinMode { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };
-
-struct LinArgs {
-    const uint16_t *x, *W, *dz;
-    const float *bias;
-    const uint16_t *residual;
-    uint16_t *out, *z;
-    const int32_t *offsets;
-    int rows, d_in, d_out, E;
-    uint32_t *status;
-};
-
-constexpr int kT = 64, kTk = 16;
-
-template <int MODE, int ACT>
-__global__ void __launch_bounds__(256) k_linear_simt(const LinArgs p)
-{
-    __shared__ GroupSmem G;
-    __shared__ float sa[kTk][kT + 1], sb[kTk][kT + 1];
-    build_groups(G, p.offsets, p.E, p.rows, kT, p.status);
-    int e, r0, r1;
-    if (MODE == LIN_DW) {
-        e = blockIdx.z;
-        r0 = G.row0[e];
-        r1 = G.row0[e + 1];
-    } else {
-        const int item = blockIdx.y;
-        if (item >= G.first[p.E])
-            return;
-        e = item_group(G, p.E, item);
-        r0 = G.row0[e] + (item - G.first[e]) * kT;
-        r1 = min(r0 + kT, G.row0[e + 1]);
-    }
-    const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
-    const int m0 = blockIdx.x * kT;
-    const int c0 = MODE == LIN_DW ? blockIdx.y * kT : r0;
-    const int c1 = MODE == LIN_DW ? min(c0 + kT, p.d_out) : r1;
-    const int K = MODE == LIN_FWD ? p.d_in : MODE == LIN_DX ? p.d_out : r1 - r0;
-    const uint16_t *We = p.W + (MODE == LIN_DW ? 0 : (long long)e * p.d_out * p.d_in);
-    const int tm = threadIdx.x & 15, tc = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    auto bf = [](uint16_t v) { return __uint_as_float((uint32_t)v << 16); };
-    for (int k0 = 0; k0 < K; k0 += kTk) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTk * kT; i += 256) {
-            int kk, mm;
-            if (MODE == LIN_FWD)
-                kk = i % kTk, mm = i / kTk;
-            else
-                kk = i / kT, mm = i % kT;
-            float a = 0.f, b = 0.f;
-            const int k = k0 + kk, m = m0 + mm;
-            if (k < K && m < M)
-                a = MODE == LIN_FWD  ? bf(We[(long long)m * p.d_in + k])
-                    : MODE == LIN_DX ? bf(We[(long long)k * p.d_in + m])
-                                     : bf(p.x[(long long)(r0 + k) * p.d_in + m]);
-            sa[kk][mm] = a;
-            int kb, cc;
-            if (MODE == LIN_DW)
-                kb = i / kT, cc = i % kT;
-            else
-                kb = i % kTk, cc = i / kTk;
-            if (k0 + kb < K && c0 + cc < c1)
-                b = MODE == LIN_FWD  ? bf(p.x[(long long)(c0 + cc) * p.d_in + k0 + kb])
-                    : MODE == LIN_DX ? bf(p.dz[(long long)(c0 + cc) * p.d_out + k0 + kb])
-                                     : bf(p.dz[(long long)(r0 + k0 + kb) * p.d_out + c0 + cc]);
-            sb[kb][cc] = b;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < kTk; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(sa[kk][tm + 16 * i], sb[kk][tc + 16 * j], acc[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + tm + 16 * i, c = c0 + tc + 16 * j;
-            if (m >= M || c >= c1)
-                continue;
-            const long long at = (MODE == LIN_DW ? (long long)e * p.d_out * p.d_in : 0) +
-                                 (long long)c * M + m;
-            float v = acc[i][j];
-            if (MODE == LIN_FWD) {
-                if (p.bias)
-                    v += p.bias[(long long)e * p.d_out + m];
-                if (p.z)
-                    p.z[at] = (uint16_t)pack_bf16x2(v, 0.f);
-                v = act_f<ACT>(v);
-                if (p.residual)
-                    v += bf(p.residual[at]);
-            }
-            p.out[at] = (uint16_t)pack_bf16x2(v, 0.f);
-        }
-}
-
-template <int MODE, int ACT>
-int launch_product(const LinArgs &p, cudaStream_t st)
-{
-    const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
-    const dim3 grid((M + kT - 1) / kT,
-                    MODE == LIN_DW ? (p.d_out + kT - 1) / kT
-                                   : (p.rows + kT - 1) / kT + std::min(p.E, p.rows),
-                    MODE == LIN_DW ? p.E : 1);
-    k_linear_simt<MODE, ACT><<<grid, 256, 0, st>>>(p);
-    return launched();
-}
-
 // ---------------------------------------------------------------- host side
 
 int check_linear(const moe_linear_t *s)
@@ -245,7 +130,8 @@ long long dz_items(const moe_linear_t &s)
 }
 
 struct LinWs {
-    size_t dz, part, total;
+    size_t dz, part, dw_part, total;
+    int splits;
 };
 
 LinWs lin_ws(const moe_linear_t &s)
@@ -259,6 +145,8 @@ LinWs lin_ws(const moe_linear_t &s)
     };
     L.dz = take(s.act != MOE_ACT_NONE ? (size_t)s.rows * s.d_out * 2 : 0);
     L.part = take((size_t)dz_items(s) * s.d_out * 4);
+    L.splits = lin_dw_splits(s);
+    L.dw_part = take(L.splits > 1 ? (size_t)L.splits * s.E * s.d_out * s.d_in * 4 : 0);
     L.total = std::max<size_t>(off, 256);
     return L;
 }
@@ -272,17 +160,6 @@ int launch_dz(const moe_linear_t &s, const uint16_t *dy, const uint16_t *z, uint
                   reinterpret_cast<const uint4 *>(z), reinterpret_cast<uint4 *>(dz), part, offsets,
                   s.E, s.rows, s.d_out, status);
     return launched();
-}
-
-int forward_product(int act, const LinArgs &p, cudaStream_t st)
-{
-    switch (act) {
-    case MOE_ACT_NONE: return launch_product<LIN_FWD, MOE_ACT_NONE>(p, st);
-    case MOE_ACT_RELU: return launch_product<LIN_FWD, MOE_ACT_RELU>(p, st);
-    case MOE_ACT_GELU: return launch_product<LIN_FWD, MOE_ACT_GELU>(p, st);
-    case MOE_ACT_GELU_TANH: return launch_product<LIN_FWD, MOE_ACT_GELU_TANH>(p, st);
-    default: return launch_product<LIN_FWD, MOE_ACT_SILU>(p, st);
-    }
 }
 
 int elementwise_backward(const moe_linear_t &s, const uint16_t *dy, const uint16_t *z,
@@ -347,8 +224,9 @@ int moe_linear_forward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.d_in = s.d_in;
     p.d_out = s.d_out;
     p.E = s.E;
+    p.act = s.act;
     p.status = status;
-    return forward_product(s.act, p, reinterpret_cast<cudaStream_t>(stream));
+    return launch_linear(LIN_FWD, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
@@ -406,12 +284,14 @@ int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.status = status;
     if (dx) {
         p.out = dx;
-        if ((rc = launch_product<LIN_DX, MOE_ACT_NONE>(p, st)))
+        if ((rc = launch_linear(LIN_DX, p, st)))
             return rc;
     }
     if (dW) {
         p.out = dW;
-        if ((rc = launch_product<LIN_DW, MOE_ACT_NONE>(p, st)))
+        p.splits = L.splits;
+        p.part = reinterpret_cast<float *>(w + L.dw_part);
+        if ((rc = launch_linear(LIN_DW, p, st)))
             return rc;
     }
     return MOE_OK;

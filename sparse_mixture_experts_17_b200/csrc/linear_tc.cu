@@ -1,0 +1,891 @@
+// linear_tc.cu -- the products of the linear layers on the 5th-generation
+// tensor cores (tcgen05, operands by TMA, accumulators in TMEM):
+//   out[c, m] = sum_k A[m, k] B[c, k],   m contiguous in the output.
+//
+// Orientation. The weight side (or, for dW, the input features) is the M side
+// of the MMA and the tokens (for dW the output features) its N side, because N
+// is free in steps of 16: a group's rows are cut into near-equal tiles of at
+// most 256 and each tile runs MMAs just wide enough, so a ragged group pays for
+// at most 31 rows that it does not have. It also puts consecutive m in
+// consecutive TMEM lanes: a warp stores 64 contiguous bytes per token, the bias
+// is one value per thread, and a token's validity is uniform over the warp.
+//
+// Operands. Every box that the TMA brings is 64 elements (128 bytes) wide,
+// 128-byte swizzled. Where the contraction runs along the contiguous axis the
+// tile is K-major; where it runs across rows (W for dx; x and dz for dW) the
+// same boxes are an MN-major operand, so nothing is ever transposed in memory.
+// W is a three-dimensional map (d_in, d_out, expert): what lies past an edge of
+// one expert's matrix reads as zero and never as the next expert's values. For
+// dW the contraction runs over a group's rows: the rows of the last block that
+// belong to the next group (or to nobody) are zeroed in shared memory, in both
+// operands, since they may hold infinities.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "linear.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBox = 64;                    // box width in elements, and the K stage
+constexpr int kBoxBytes = kBox * kBox * 2;  // 64 rows of 128 bytes
+constexpr int kTileC = 256;                 // widest N
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ void tma_3d(void *dst, const void *tmap, int c0, int c1, int c2,
+                                       uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_3d_pair(void *dst, const void *tmap, int c0, int c1, int c2,
+                                            uint32_t bar_cluster)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
+        : "memory");
+}
+
+// Arrive on a barrier of the cluster and add to the bytes that it waits for.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// Make generic-proxy writes to shared memory visible to the MMAs.
+__device__ __forceinline__ void fence_proxy_async()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// MN-major operand in 128-byte-swizzled boxes of 64 (MN) x 64 (K): 8 K rows of
+// 128 bytes per 1024-byte atom (stride offset 1024 between atoms along K), the
+// next 64 MN elements one box further (leading offset 8192).
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t smem_addr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(kBoxBytes >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Operand descriptor of K step kk (16 elements) of a stage.
+template <bool MN>
+__device__ __forceinline__ uint64_t op_desc(uint32_t base, int kk)
+{
+    return MN ? smem_desc_mn128(base + kk * 2048) : smem_desc_k128(base + kk * 32);
+}
+
+template <LinMode MODE>
+__device__ __forceinline__ uint32_t lin_idesc(int M, int N)
+{
+    return idesc_bf16_f32(M, N) | (MODE != LIN_FWD ? 1u << 15 : 0u)   // A is MN-major
+           | (MODE == LIN_DW ? 1u << 16 : 0u);                        // B is MN-major
+}
+
+// ---------------------------------------------------------------- epilogue
+
+struct LinOut {
+    const float *bias;
+    const uint16_t *residual;
+    uint16_t *out, *z;
+    float *part;        // LIN_DW in splits: fp32 sums instead of out
+    long long ld;       // elements between consecutive c
+};
+
+// Columns [0, n) of one lane's accumulator row, n <= 32: output elements
+// (c0 + j, m). `at` = c0 * ld + m.
+template <LinMode MODE, int ACT>
+__device__ __forceinline__ void store_chunk(const LinOut &o, const float (&v)[32],
+                                            const uint16_t (&res)[32], float bias, long long at, int n)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (j < n) {
+            const long long i = at + j * o.ld;
+            float f = v[j];
+            if (MODE == LIN_FWD) {
+                f += bias;
+                if (o.z)
+                    o.z[i] = (uint16_t)pack_bf16x2(f, 0.f);
+                f = act_f<ACT>(f);
+                if (o.residual)
+                    f += __uint_as_float((uint32_t)res[j] << 16);
+            }
+            if (MODE == LIN_DW && o.part)
+                o.part[i] = f;
+            else
+                o.out[i] = (uint16_t)pack_bf16x2(f, 0.f);
+        }
+    }
+}
+
+template <LinMode MODE>
+__device__ __forceinline__ void load_residual(const LinOut &o, uint16_t (&res)[32], long long at, int n)
+{
+    if (MODE == LIN_FWD && o.residual) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            res[j] = j < n ? o.residual[at + j * o.ld] : (uint16_t)0;
+    }
+}
+
+// ---------------------------------------------------------------- pair kernel
+// Persistent; a cluster of two CTAs computes tiles of 256 (m) x up to 256 (c)
+// with cta_group::2 MMAs that the leader issues: each CTA loads its own 128 m
+// of A and its own half of the tile's c of B. Two accumulators of 256 TMEM
+// columns alternate, so a tile's epilogue overlaps the next tile's main loop.
+//   warp 0   producer        warp 1   MMA issue (leader)
+//   warp 2   dW: zeroes the rows of a group's last block past its end
+//   warps 4-11  epilogue, two per TMEM lane quarter, alternating 32 columns
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 6;
+constexpr int kPairABytes = 2 * kBoxBytes;
+constexpr int kPairStage = 4 * kBoxBytes;   // A and B halves of one CTA
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256;
+
+struct PairArgs {
+    const int32_t *offsets;
+    int E, rows, d_in, d_out;
+    int m_tiles;     // tiles of 256 along m
+    int c_tiles;     // LIN_DW: tiles of 256 along d_out
+    int kblocks;     // LIN_FWD, LIN_DX
+    int band;        // items of a group whose B rows stay in L2 while W passes by
+    int splits;      // LIN_DW
+    LinOut o;
+    uint32_t *status;
+};
+
+struct TileAt {
+    int e, m0;        // group, first m
+    int c0, cn;       // first c (a row, or an output feature) and how many
+    int r0;           // LIN_DW: first row of the contraction
+    int nkb, tail;    // K blocks; LIN_DW: rows of the last block (0: all 64)
+    int split;
+};
+
+// Rows of one token tile of a group of n rows: near-equal tiles of at most 256,
+// a multiple of 32. Never leaves a tile empty: 256 (tiles - 1) < n.
+__device__ __forceinline__ int tile_rows(int n)
+{
+    const int nt = (n + kTileC - 1) / kTileC;
+    return ((n + nt - 1) / nt + 31) & ~31;
+}
+
+template <LinMode MODE>
+__device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G, int t)
+{
+    TileAt a;
+    if (MODE == LIN_DW) {
+        const int per = p.m_tiles * p.c_tiles;
+        const int g = t / per, r = t - g * per;
+        a.e = g / p.splits;
+        a.split = g - a.e * p.splits;
+        a.m0 = (r % p.m_tiles) * 256;
+        a.c0 = (r / p.m_tiles) * kTileC;
+        a.cn = min(kTileC, p.d_out - a.c0);
+        const int first = G.row0[a.e], n = G.row0[a.e + 1] - first;
+        const int all = (n + kBox - 1) / kBox, part = (all + p.splits - 1) / p.splits;
+        const int k0 = min(a.split * part, all), k1 = min(k0 + part, all);
+        a.nkb = k1 - k0;
+        a.r0 = first + k0 * kBox;
+        a.tail = (k1 == all && k1 > k0) ? n - (all - 1) * kBox : 0;
+        if (a.tail == kBox)
+            a.tail = 0;
+    } else {
+        const int it = t / p.m_tiles;
+        a.e = item_group(G, p.E, it);
+        const int f = G.first[a.e], ni = G.first[a.e + 1] - f;
+        const int local = t - f * p.m_tiles;
+        const int per = p.band * p.m_tiles;
+        const int b = local / per, r = local - b * per;
+        const int in_band = min(p.band, ni - b * p.band);
+        const int i = b * p.band + r % in_band;
+        a.m0 = (r / in_band) * 256;
+        const int first = G.row0[a.e], n = G.row0[a.e + 1] - first;
+        const int q = tile_rows(n);
+        a.c0 = first + i * q;
+        a.cn = min(q, n - i * q);
+        a.nkb = p.kblocks;
+        a.r0 = 0;
+        a.tail = 0;
+        a.split = 0;
+    }
+    return a;
+}
+
+template <LinMode MODE, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const PairArgs p)
+{
+    constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GroupSmem G;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStage);
+    uint64_t *empty = full + kPairStages;
+    uint64_t *tfull = empty + kPairStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *tailbar = tempty + 2;   // one a stage: several last blocks may be in flight
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tailbar + kPairStages);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 2);    // one arrival of each CTA, with its bytes
+            mbar_init(&empty[s], 1);
+            mbar_init(&tailbar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 16);   // 8 epilogue warps of each CTA
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();
+    pdl_trigger();
+    // items of one group: token tiles; LIN_DW needs the groups' rows only
+    build_groups(G, p.offsets, p.E, p.rows, kTileC, p.status);
+    tc_fence_before();
+    cluster_sync_all();   // both CTAs' barriers exist and TMEM is allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = MODE == LIN_DW ? p.E * p.splits * p.m_tiles * p.c_tiles
+                                     : G.first[p.E] * p.m_tiles;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {   // ---------------- producer (both CTAs)
+            uint32_t it = 0;
+            for (int t = pair; t < total; t += npairs) {
+                const TileAt a = tile_at<MODE>(p, G, t);
+                const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
+                const int nb = (half + kBox - 1) / kBox;
+                const int c0 = a.c0 + (int)rank * half, m0 = a.m0 + 128 * (int)rank;
+                const uint32_t bytes = kPairABytes + nb * kBoxBytes;
+                bool ok = true;
+                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    const uint32_t ph = (it / kPairStages) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + s * kPairStage, *sb = sa + kPairABytes;
+                    const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
+                    uint32_t bar;
+                    if (tail) {   // to this CTA's own barrier; warp 2 passes it on
+                        mbar_arrive_expect_tx(&tailbar[s], bytes);
+                        bar = mapa_shared(smem_u32(&tailbar[s]), rank);
+                    } else {
+                        bar = mapa_shared(smem_u32(&full[s]), 0);
+                        mbar_arrive_expect_tx_cluster(bar, bytes);
+                    }
+                    const int k = kb * kBox;
+                    if (MODE == LIN_FWD) {
+                        tma_3d_pair(sa, &tmA, k, m0, a.e, bar);
+                    } else if (MODE == LIN_DX) {
+                        tma_3d_pair(sa, &tmA, m0, k, a.e, bar);
+                        tma_3d_pair(sa + kBoxBytes, &tmA, m0 + kBox, k, a.e, bar);
+                    } else {
+                        tma_load_2d_pair(sa, &tmA, m0, a.r0 + k, bar);
+                        tma_load_2d_pair(sa + kBoxBytes, &tmA, m0 + kBox, a.r0 + k, bar);
+                    }
+                    for (int j = 0; j < nb; ++j) {
+                        if (MODE == LIN_DW)
+                            tma_load_2d_pair(sb + j * kBoxBytes, &tmB, c0 + j * kBox, a.r0 + k, bar);
+                        else
+                            tma_load_2d_pair(sb + j * kBoxBytes, &tmB, k, c0 + j * kBox, bar);
+                    }
+                }
+                if (!ok)
+                    break;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {   // ---------------- MMA issue
+            uint32_t it = 0, local = 0;
+            for (int t = pair; t < total; t += npairs) {
+                const TileAt a = tile_at<MODE>(p, G, t);
+                if (MODE == LIN_DW && a.nkb == 0)
+                    continue;            // nothing to add up: the epilogue writes zeros
+                const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
+                ++local;
+                const uint32_t idesc = lin_idesc<MODE>(256, (a.cn + 31) & ~31);
+                if (!mbar_wait_cluster(&tempty[b], aph ^ 1u, abort_flag, p.status))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + b * kTileC;
+                bool ok = true;
+                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    const uint32_t ph = (it / kPairStages) & 1u;
+                    if (!mbar_wait_cluster(&full[s], ph, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(smem + s * kPairStage), b0 = a0 + kPairABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBox / 16; ++kk)
+                        tc_mma_bf16_pair(d, op_desc<A_MN>(a0, kk), op_desc<B_MN>(b0, kk), idesc,
+                                         (kb | kk) != 0);
+                    tc_commit_pair(&empty[s], 0x3);
+                }
+                if (!ok)
+                    break;
+                tc_commit_pair(&tfull[b], 0x3);
+            }
+        }
+    } else if (MODE == LIN_DW && warp == 2) {   // ---------------- last blocks (both CTAs)
+        uint32_t it = 0, phases = 0;   // bit s: parity of stage s's next use
+        for (int t = pair; t < total; t += npairs) {
+            const TileAt a = tile_at<MODE>(p, G, t);
+            it += a.nkb;
+            if (!a.tail)
+                continue;
+            const int s = (it - 1) % kPairStages;
+            if (!__all_sync(kFullMask, mbar_wait(&tailbar[s], (phases >> s) & 1u, abort_flag, p.status)))
+                break;
+            phases ^= 1u << s;
+            // row r of a 64 x 64 box is its bytes [128 r, 128 r + 128): the swizzle
+            // only permutes the 16-byte pieces of a row
+            const int per = (kBox - a.tail) * 8;
+            const int nb = (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
+            uint8_t *sa = smem + s * kPairStage;
+            for (int i = lane; i < (2 + nb) * per; i += 32)
+                reinterpret_cast<uint4 *>(sa + (i / per) * kBoxBytes + a.tail * 128)[i % per] =
+                    make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+        }
+    } else if (warp >= 4) {   // ---------------- epilogue (both CTAs)
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
+        uint32_t local = 0;
+        for (int t = pair; t < total; t += npairs) {
+            const TileAt a = tile_at<MODE>(p, G, t);
+            const int m = a.m0 + 128 * (int)rank + q * 32 + lane;
+            const bool ok = m < M;
+            const long long base =
+                MODE == LIN_DW ? ((long long)(p.o.part ? a.split * p.E : 0) + a.e) * p.d_out * p.o.ld
+                               : 0;
+            const bool none = MODE == LIN_DW && a.nkb == 0;
+            const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
+            float bias = 0.f;
+            if (MODE == LIN_FWD && p.o.bias && ok)
+                bias = p.o.bias[(long long)a.e * p.d_out + m];
+            if (!none) {
+                if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
+                    break;
+                ++local;
+                tc_fence_after();
+            }
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kTileC;
+#pragma unroll 1
+            for (int c = h * 32; c < a.cn; c += 64) {
+                const int n = min(32, a.cn - c);
+                const long long at = base + (long long)(a.c0 + c) * p.o.ld + m;
+                float v[32];
+                uint16_t res[32];
+                if (none) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = 0.f;
+                } else {
+                    tmem_ld32(tb + c, v);
+                }
+                if (ok)
+                    load_residual<MODE>(p.o, res, at, n);
+                if (!none)
+                    tmem_ld_wait();
+                if (ok)
+                    store_chunk<MODE, ACT>(p.o, v, res, bias, at, n);
+            }
+            if (!none) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));
+            }
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag) {   // a wait ran out: let this CTA's copies in flight land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull)
+            ;
+    }
+    tc_fence_before();
+    cluster_sync_all();   // neither CTA leaves while the pair's MMAs may read its memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- split kernel
+// For few tiles (one token, small batches, small layers): one CTA per 128 (m) x
+// up to BC (c) x a slice of K; the S CTAs of a cluster split K and add their
+// accumulators through distributed shared memory in rank order (no atomics, no
+// workspace). Not persistent: with BC <= 128 two CTAs share an SM, so one's
+// start and end hide behind the other's loads.
+template <int BC>
+struct SplitCfg {
+    static constexpr int BOXROWS = BC < 64 ? BC : 64;
+    static constexpr int A_BYTES = 2 * kBoxBytes;
+    static constexpr int B_BYTES = BC * 128;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BC == 32 ? 5 : BC == 128 ? 3 : 4;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+    static_assert(BC * 128 * 4 <= STAGES * STAGE, "the partial sums reuse the ring");
+};
+
+struct SplitArgs {
+    const int32_t *offsets;
+    int E, rows, d_in, d_out;
+    int S;
+    int kblocks;
+    LinOut o;
+    uint32_t *status;
+};
+
+template <LinMode MODE, int ACT, int BC>
+__global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
+    k_linear_split(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const SplitArgs p)
+{
+    using C = SplitCfg<BC>;
+    constexpr bool A_MN = MODE == LIN_DX;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ GroupSmem G;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::STAGES * C::STAGE);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *done = empty + C::STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % p.S;   // clusters run along x
+    const int m0 = (blockIdx.x / p.S) * 128;
+    pdl_wait();
+    pdl_trigger();
+    build_groups(G, p.offsets, p.E, p.rows, BC, p.status);
+    const int item = blockIdx.y;
+    if (item >= G.first[p.E])
+        return;                          // the whole cluster: it has one blockIdx.y
+    const int e = item_group(G, p.E, item);
+    const int c0 = G.row0[e] + (item - G.first[e]) * BC;
+    const int cn = min(BC, G.row0[e + 1] - c0);
+    const int per = (p.kblocks + p.S - 1) / p.S;
+    const int k0 = min(rank * per, p.kblocks), nkb = min(k0 + per, p.kblocks) - k0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, BC);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0 && lane == 0) {   // ---------------- producer
+        const int nb = (cn + C::BOXROWS - 1) / C::BOXROWS;
+        const uint32_t bytes = C::A_BYTES + nb * C::BOXROWS * 128;
+        for (int i = 0; i < nkb; ++i) {
+            const int s = i % C::STAGES;
+            if (!mbar_wait(&empty[s], ((i / C::STAGES) & 1u) ^ 1u, abort_flag, p.status))
+                break;
+            uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
+            mbar_arrive_expect_tx(&full[s], bytes);
+            const int k = (k0 + i) * kBox;
+            if (A_MN) {
+                tma_3d(sa, &tmA, m0, k, e, &full[s]);
+                tma_3d(sa + kBoxBytes, &tmA, m0 + kBox, k, e, &full[s]);
+            } else {
+                tma_3d(sa, &tmA, k, m0, e, &full[s]);
+            }
+            for (int j = 0; j < nb; ++j)
+                tma_load_2d(sb + j * C::BOXROWS * 128, &tmB, k, c0 + j * C::BOXROWS, &full[s]);
+        }
+    } else if (warp == 1 && lane == 0) {   // ---------------- MMA issue
+        const uint32_t idesc = lin_idesc<MODE>(128, (cn + 15) & ~15);
+        bool ok = true;
+        for (int i = 0; i < nkb; ++i) {
+            const int s = i % C::STAGES;
+            if (!mbar_wait(&full[s], (i / C::STAGES) & 1u, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(smem + s * C::STAGE), b0 = a0 + C::A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < kBox / 16; ++kk)
+                tc_mma_bf16(tmem_base, op_desc<A_MN>(a0, kk), op_desc<false>(b0, kk), idesc,
+                            (i | kk) != 0);
+            tc_commit(&empty[s]);
+        }
+        if (ok)
+            tc_commit(done);
+    }
+    __syncwarp();
+
+    // ---------------- epilogue: all eight warps, two per TMEM lane quarter
+    const bool got = __all_sync(kFullMask, mbar_wait(done, 0, abort_flag, p.status));
+    tc_fence_after();
+    const int q = warp & 3, h = warp >> 2;
+    const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    if (p.S == 1) {
+        const int m = m0 + q * 32 + lane;
+        const float bias = (MODE == LIN_FWD && p.o.bias && m < M) ? p.o.bias[(long long)e * p.d_out + m] : 0.f;
+#pragma unroll 1
+        for (int c = h * 32; got && c < cn; c += 64) {
+            const int n = min(32, cn - c);
+            const long long at = (long long)(c0 + c) * p.o.ld + m;
+            float v[32];
+            uint16_t res[32];
+            tmem_ld32(tb + c, v);
+            if (m < M)
+                load_residual<MODE>(p.o, res, at, n);
+            tmem_ld_wait();
+            if (m < M)
+                store_chunk<MODE, ACT>(p.o, v, res, bias, at, n);
+        }
+    } else {
+        // partial sums [c][128 m] over the ring, which every copy and MMA has left
+        float *mine = reinterpret_cast<float *>(smem);
+#pragma unroll 1
+        for (int c = h * 32; got && c < cn; c += 64) {
+            float v[32];
+            if (nkb > 0) {
+                tmem_ld32(tb + c, v);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < cn)
+                    mine[(c + j) * 128 + q * 32 + lane] = v[j];
+        }
+        __syncwarp();
+        cluster_sync_all();
+        // each CTA finishes 128 / S of the m of every token
+        const int mw = 128 / p.S;
+        uint32_t peer[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            peer[r] = r < p.S ? mapa_shared(smem_u32(mine), r) : 0u;
+        if (got)
+            for (int i = threadIdx.x; i < cn * mw; i += 256) {
+                const int c = i / mw, ml = rank * mw + i % mw, m = m0 + ml;
+                if (m >= M)
+                    continue;
+                float f = 0.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < p.S) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(v)
+                                     : "r"(peer[r] + (uint32_t)(c * 128 + ml) * 4u));
+                        f += v;
+                    }
+                const long long at = (long long)(c0 + c) * p.o.ld + m;
+                if (MODE == LIN_FWD) {
+                    if (p.o.bias)
+                        f += p.o.bias[(long long)e * p.d_out + m];
+                    if (p.o.z)
+                        p.o.z[at] = (uint16_t)pack_bf16x2(f, 0.f);
+                    f = act_f<ACT>(f);
+                    if (p.o.residual)
+                        f += __uint_as_float((uint32_t)p.o.residual[at] << 16);
+                }
+                p.o.out[at] = (uint16_t)pack_bf16x2(f, 0.f);
+            }
+        __syncwarp();
+        cluster_sync_all();   // no CTA leaves while another reads its sums
+    }
+    if (*abort_flag) {   // a wait ran out: let this CTA's copies in flight land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull)
+            ;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, BC);
+    }
+}
+
+// dW = bf16(sum over the splits, in order).
+__global__ void __launch_bounds__(256)
+    k_linear_dw_sum(const float4 *__restrict__ part, uint2 *__restrict__ dW, long long n4, int splits)
+{
+    pdl_wait();
+    pdl_trigger();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4)
+        return;
+    float4 s = part[i];
+    for (int k = 1; k < splits; ++k) {
+        const float4 v = part[i + k * n4];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    dW[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// bf16 [depth, rows, cols] (depth 0: two-dimensional); boxes of 64 x box_rows
+// elements, 128-byte swizzle, zero fill outside.
+int make_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long depth,
+             int box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return MOE_ERR_CUDA;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+    cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
+    cuuint32_t box[3] = {(cuuint32_t)kBox, (cuuint32_t)box_rows, 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth ? 3 : 2,
+                          const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <class K>
+int allow_smem(K kernel, int bytes)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+LinOut out_of(LinMode mode, const LinArgs &a)
+{
+    LinOut o;
+    std::memset(&o, 0, sizeof o);
+    o.bias = a.bias;
+    o.residual = a.residual;
+    o.out = a.out;
+    o.z = a.z;
+    o.part = (mode == LIN_DW && a.splits > 1) ? a.part : nullptr;
+    o.ld = mode == LIN_FWD ? a.d_out : a.d_in;
+    return o;
+}
+
+// Maps of the two operands. A: W [E, d_out, d_in] (box 128 rows when K-major, 64
+// when MN-major), or x for dW. B: the rows of x or dz.
+int operand_maps(LinMode mode, const LinArgs &a, int b_box_rows, CUtensorMap *A, CUtensorMap *B)
+{
+    int rc = mode == LIN_DW ? make_map(A, a.x, a.d_in, a.rows, 0, kBox)
+                            : make_map(A, a.W, a.d_in, a.d_out, a.E, mode == LIN_FWD ? 128 : kBox);
+    if (rc)
+        return rc;
+    return mode == LIN_FWD ? make_map(B, a.x, a.d_in, a.rows, 0, b_box_rows)
+                           : make_map(B, a.dz, a.d_out, a.rows, 0, b_box_rows);
+}
+
+template <LinMode MODE, int ACT>
+int launch_pair(const LinArgs &a, cudaStream_t st)
+{
+    CUtensorMap A, B;
+    int rc = operand_maps(MODE, a, kBox, &A, &B);
+    if (rc || (rc = allow_smem(k_linear_pair<MODE, ACT>, kPairSmem)))
+        return rc;
+    PairArgs p;
+    std::memset(&p, 0, sizeof p);
+    p.offsets = a.offsets;
+    p.E = a.E;
+    p.rows = a.rows;
+    p.d_in = a.d_in;
+    p.d_out = a.d_out;
+    p.m_tiles = ceil_div(MODE == LIN_FWD ? a.d_out : a.d_in, 256);
+    p.c_tiles = ceil_div(a.d_out, kTileC);
+    const int K = MODE == LIN_FWD ? a.d_in : a.d_out;
+    p.kblocks = ceil_div(K, kBox);
+    // a band's token rows stay in L2 (48 MiB of them) while it sweeps the m tiles
+    p.band = (int)std::max<long long>((48LL << 20) / ((long long)kTileC * K * 2), 1);
+    p.splits = std::max(a.splits, 1);
+    p.o = out_of(MODE, a);
+    p.status = a.status;
+    const long long tiles =
+        MODE == LIN_DW ? (long long)a.E * p.splits * p.m_tiles * p.c_tiles
+                       : (long long)(ceil_div(a.rows, kTileC) + std::min(a.E, a.rows)) * p.m_tiles;
+    const int pairs = (int)std::min<long long>(tiles, num_sms() / 2);
+    launch_pdl_ex(k_linear_pair<MODE, ACT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, A, B, p);
+    if ((rc = launched()))
+        return rc;
+    if (MODE == LIN_DW && p.splits > 1) {
+        const long long n4 = (long long)a.E * a.d_out * a.d_in / 4;
+        launch_pdl_ex(k_linear_dw_sum, dim3(ceil_div(n4, 256)), dim3(256), 0, st,
+                      reinterpret_cast<const float4 *>(a.part), reinterpret_cast<uint2 *>(a.out), n4,
+                      p.splits);
+        return launched();
+    }
+    return MOE_OK;
+}
+
+template <LinMode MODE, int ACT, int BC>
+int launch_split(const LinArgs &a, int S, cudaStream_t st)
+{
+    using C = SplitCfg<BC>;
+    CUtensorMap A, B;
+    int rc = operand_maps(MODE, a, C::BOXROWS, &A, &B);
+    if (rc || (rc = allow_smem(k_linear_split<MODE, ACT, BC>, C::SMEM)))
+        return rc;
+    SplitArgs p;
+    std::memset(&p, 0, sizeof p);
+    p.offsets = a.offsets;
+    p.E = a.E;
+    p.rows = a.rows;
+    p.d_in = a.d_in;
+    p.d_out = a.d_out;
+    p.S = S;
+    p.kblocks = ceil_div(MODE == LIN_FWD ? a.d_in : a.d_out, kBox);
+    p.o = out_of(MODE, a);
+    p.status = a.status;
+    const int m_tiles = ceil_div(MODE == LIN_FWD ? a.d_out : a.d_in, 128);
+    // a group of n rows has at most n / BC + 1 items, and none when it is empty
+    const int items = a.offsets ? a.rows / BC + std::min(a.E, a.rows) : ceil_div(a.rows, BC);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(m_tiles * S, items);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, k_linear_split<MODE, ACT, BC>, A, B, p);
+    return launched();
+}
+
+// Engine and shape of one product over token rows.
+template <LinMode MODE, int ACT>
+int launch_rows(const LinArgs &a, cudaStream_t st)
+{
+    const int M = MODE == LIN_FWD ? a.d_out : a.d_in, K = MODE == LIN_FWD ? a.d_in : a.d_out;
+    const int groups = std::min(a.E, a.rows);
+    const int avg = ceil_div(a.rows, groups);
+    const long long pair_tiles = (long long)groups * ceil_div(avg, kTileC) * ceil_div(M, 256);
+    const int sms = num_sms();
+    if (pair_tiles >= sms / 2 && avg > 32)
+        return launch_pair<MODE, ACT>(a, st);
+    const int bc = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
+    const long long tiles = (long long)groups * ceil_div(avg, bc) * ceil_div(M, 128);
+    // CTAs that split K: enough to fill the SMs, each with four K stages or more
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= (bc == 256 ? sms : 2 * sms) && ceil_div(K, kBox) >= 2 * S * 4)
+        S *= 2;
+    switch (bc) {
+    case 32: return launch_split<MODE, ACT, 32>(a, S, st);
+    case 64: return launch_split<MODE, ACT, 64>(a, S, st);
+    case 128: return launch_split<MODE, ACT, 128>(a, S, st);
+    default: return launch_split<MODE, ACT, 256>(a, S, st);
+    }
+}
+
+} // namespace
+
+int lin_dw_splits(const moe_linear_t &s)
+{
+    const long long tiles = (long long)s.E * ceil_div(s.d_in, 256) * ceil_div(s.d_out, kTileC);
+    const long long room = num_sms() / std::max<long long>(tiles, 1);
+    return (int)std::max<long long>(1, std::min<long long>({room, 16LL, (long long)s.rows / 512}));
+}
+
+int launch_linear(LinMode mode, const LinArgs &a, cudaStream_t st)
+{
+    if (mode == LIN_DX)
+        return launch_rows<LIN_DX, MOE_ACT_NONE>(a, st);
+    if (mode == LIN_DW)
+        return launch_pair<LIN_DW, MOE_ACT_NONE>(a, st);
+    switch (a.act) {
+    case MOE_ACT_NONE: return launch_rows<LIN_FWD, MOE_ACT_NONE>(a, st);
+    case MOE_ACT_RELU: return launch_rows<LIN_FWD, MOE_ACT_RELU>(a, st);
+    case MOE_ACT_GELU: return launch_rows<LIN_FWD, MOE_ACT_GELU>(a, st);
+    case MOE_ACT_GELU_TANH: return launch_rows<LIN_FWD, MOE_ACT_GELU_TANH>(a, st);
+    default: return launch_rows<LIN_FWD, MOE_ACT_SILU>(a, st);
+    }
+}
+
+} // namespace moe
