@@ -61,14 +61,6 @@ __device__ __forceinline__ void tma_3d_pair(void *dst, const void *tmap, int c0,
         : "memory");
 }
 
-// Arrive on a barrier of the cluster and add to the bytes that it waits for.
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
-}
-
 // Make generic-proxy writes to shared memory visible to the MMAs.
 __device__ __forceinline__ void fence_proxy_async()
 {
@@ -257,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
-            mbar_init(&full[s], 2);    // one arrival of each CTA, with its bytes
+            mbar_init(&full[s], 2);    // the leader's producer twice, or each CTA's warp 2 once
             mbar_init(&empty[s], 1);
             mbar_init(&tailbar[s], 1);
         }
@@ -313,7 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         bar = mapa_shared(smem_u32(&tailbar[s]), rank);
                     } else {
                         bar = mapa_shared(smem_u32(&full[s]), 0);
-                        mbar_arrive_expect_tx_cluster(bar, bytes);
+                        if (leader) {   // for both CTAs' copies: halves are equal
+                            mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                            mbar_arrive(&full[s]);
+                        }
                     }
                     const int k = kb * kBox;
                     if (MODE == LIN_FWD) {
@@ -354,7 +349,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                     const int s = it % kPairStages;
                     const uint32_t ph = (it / kPairStages) & 1u;
-                    if (!mbar_wait_cluster(&full[s], ph, abort_flag, p.status)) {
+                    // Copies need no acquire beyond this CTA. One at cluster scope
+                    // stalls the issue for longer than a stage's MMAs take, so only
+                    // a last block, whose zeros the peer wrote, waits with it.
+                    const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
+                    if (!(tail ? mbar_wait_cluster(&full[s], ph, abort_flag, p.status)
+                               : mbar_wait(&full[s], ph, abort_flag, p.status))) {
                         ok = false;
                         break;
                     }
