@@ -124,7 +124,7 @@ __device__ __forceinline__ double run_sum(const uint4 (&v)[NV])
     if (any == 0)
         return 0.0;
     double d = 0.0;
-#pragma unroll 1
+#pragma unroll   // a loop would index v at run time and put it in local memory, on the fast side too
     for (int u = 0; u < NV; ++u) {
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll

@@ -14,13 +14,18 @@ namespace moe {
 struct GroupSmem {
     int row0[MOE_MAX_E + 1];    // first row of each group, so [e + 1] is the end of group e
     int first[MOE_MAX_E + 1];   // first item of each group; [E]: number of items
-    int warp[17];
+    int group[MOE_MAX_E];       // ORDER: the groups' places in first[]
+    int nbig;                   // ORDER: groups of two or more items, which come first
+    unsigned long long warp[8];
     int bad;
 };
 
 // Fills G. All threads of a block of >= 256 threads (a multiple of 32) call it;
 // the first 256 work. offsets NULL: one group of all rows. Offsets that decrease
-// or leave [0, rows] make every group empty and flag MOE_ERR_CHECK.
+// or leave [0, rows] make every group empty and flag MOE_ERR_CHECK. With ORDER,
+// first[] runs over the groups of two or more items and then over the others,
+// and group[i] is the group at place i (row0 stays by group).
+template <bool ORDER = false>
 __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offsets, int E, int rows,
                                              int item_rows, uint32_t *status)
 {
@@ -43,12 +48,16 @@ __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offset
             flag_status(status, MOE_ERR_CHECK);
     }
     const int n = (b - a + item_rows - 1) / item_rows;
-    // exclusive scan over the first 256 threads
+    // exclusive scan over the first 256 threads of the items (26 bits: at most 2^24 + 256),
+    // and with ORDER also of the big groups' items and of the big groups themselves (9 bits)
+    const bool big = ORDER && n > 1 && t < E;
+    const unsigned long long mine = (unsigned long long)n | (big ? (unsigned long long)n << 26 : 0) |
+                                    (big ? 1ull << 52 : 0);
     const int lane = t & 31, warp = t >> 5;
-    int inc = n;
+    unsigned long long inc = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(kFullMask, inc, off);
+        const unsigned long long o = __shfl_up_sync(kFullMask, inc, off);
         if (lane >= off)
             inc += o;
     }
@@ -56,20 +65,38 @@ __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offset
         G.warp[warp] = inc;
     __syncthreads();
     if (t < E) {
-        int base = 0;
-        for (int w = 0; w < warp; ++w)
-            base += G.warp[w];
-        G.first[t] = base + inc - n;
-        G.row0[t] = a;
-        if (t == E - 1) {
-            G.first[E] = base + inc;
-            G.row0[E] = b;
+        unsigned long long base = 0, sum = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w == warp)
+                base = sum;
+            sum += G.warp[w];
         }
+        const unsigned long long ex = base + inc - mine;
+        const int mask = (1 << 26) - 1;
+        const int all = (int)(ex & mask), in_big = (int)(ex >> 26) & mask, bigs = (int)(ex >> 52);
+        if (ORDER) {
+            const int nbig = (int)(sum >> 52), big_items = (int)(sum >> 26) & mask;
+            const int place = big ? bigs : nbig + t - bigs;
+            G.first[place] = big ? in_big : big_items + all - in_big;
+            G.group[place] = t;
+            if (t == 0) {
+                G.nbig = nbig;
+                G.first[E] = (int)(sum & mask);
+            }
+        } else {
+            G.first[t] = all;
+            if (t == 0)
+                G.first[E] = (int)(sum & mask);
+        }
+        G.row0[t] = a;
+        if (t == E - 1)
+            G.row0[E] = b;
     }
     __syncthreads();
 }
 
-// Group of an item (item < G.first[E]): the e with first[e] <= item < first[e+1].
+// Group of an item (item < G.first[E]): the e with first[e] <= item < first[e+1]
+// (with ORDER its place). Empty groups never come out: the last one that fits is taken.
 __device__ __forceinline__ int item_group(const GroupSmem &G, int E, int item)
 {
     int lo = 0, hi = E - 1;

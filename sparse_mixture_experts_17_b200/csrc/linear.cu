@@ -26,11 +26,12 @@ namespace {
 // CTA of 8 warps covers 256 columns (a lane 8 of them, 16-byte vectors) and
 // its warps take the item's rows in turn; their sums meet in shared memory in
 // warp order, so db repeats bit for bit.
-constexpr int kDzRows = 128;
+constexpr int kDzRows = 64;
 constexpr int kDzCols = 256;
+constexpr int kDzUnroll = 4;   // rows of a warp in flight
 
 template <int ACT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     k_linear_dz(const uint4 *__restrict__ dy, const uint4 *__restrict__ z, uint4 *dz, float *part,
                 const int32_t *offsets, int E, int rows, int d_out, uint32_t *status)
 {
@@ -49,30 +50,36 @@ __global__ void __launch_bounds__(256)
     const int col = blockIdx.x * kDzCols + lane * 8, nv = d_out / 8;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (col < d_out) {
-        for (int r = r0 + warp; r < r1; r += 8) {
-            const long long at = (long long)r * nv + col / 8;
-            const uint4 g = ld_stream_v4(dy + at);
-            const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-            uint32_t ow[4];
-            if (ACT != MOE_ACT_NONE) {
-                const uint4 zz = ld_stream_v4(z + at);
-                const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+        const long long at0 = (long long)r0 * nv + col / 8;
+        for (int r = warp; r < r1 - r0; r += 8 * kDzUnroll) {
+            uint4 g[kDzUnroll], zz[kDzUnroll];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float a = bf16lo(gw[q]) * act_grad_f<ACT>(bf16lo(zw[q]));
-                    const float b = bf16hi(gw[q]) * act_grad_f<ACT>(bf16hi(zw[q]));
-                    sum[2 * q] += a;
-                    sum[2 * q + 1] += b;
-                    ow[q] = pack_bf16x2(a, b);
+            for (int u = 0; u < kDzUnroll; ++u)
+                if (r + 8 * u < r1 - r0) {
+                    g[u] = ld_stream_v4(dy + at0 + (long long)(r + 8 * u) * nv);
+                    if (ACT != MOE_ACT_NONE)
+                        zz[u] = ld_stream_v4(z + at0 + (long long)(r + 8 * u) * nv);
                 }
-                dz[at] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    sum[2 * q] += bf16lo(gw[q]);
-                    sum[2 * q + 1] += bf16hi(gw[q]);
+            for (int u = 0; u < kDzUnroll; ++u)
+                if (r + 8 * u < r1 - r0) {
+                    const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                    const uint32_t zw[4] = {zz[u].x, zz[u].y, zz[u].z, zz[u].w};
+                    uint32_t ow[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float a = bf16lo(gw[q]), b = bf16hi(gw[q]);
+                        if (ACT != MOE_ACT_NONE) {
+                            a *= act_grad_f<ACT>(bf16lo(zw[q]));
+                            b *= act_grad_f<ACT>(bf16hi(zw[q]));
+                        }
+                        sum[2 * q] += a;
+                        sum[2 * q + 1] += b;
+                        ow[q] = pack_bf16x2(a, b);
+                    }
+                    if (ACT != MOE_ACT_NONE)
+                        dz[at0 + (long long)(r + 8 * u) * nv] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                 }
-            }
         }
     }
     if (!part)
@@ -104,6 +111,7 @@ __global__ void __launch_bounds__(256)
     if (c >= d_out)
         return;
     float s = 0.f;
+#pragma unroll 8
     for (int i = G.first[e]; i < G.first[e + 1]; ++i)
         s += part[(long long)i * d_out + c];
     db[(long long)e * d_out + c] = s;

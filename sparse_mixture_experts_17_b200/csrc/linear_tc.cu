@@ -95,6 +95,39 @@ __device__ __forceinline__ uint32_t lin_idesc(int M, int N)
            | (MODE == LIN_DW ? 1u << 16 : 0u);                        // B is MN-major
 }
 
+// 16 TMEM lanes (m) x 32 columns (c): in v[4 i + j], j = 0, 1: lane t / 4, column
+// 8 i + 2 (t % 4) + j; j = 2, 3: the same columns of lane t / 4 + 8 (t: this thread).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+// Four 8 x 8 matrices of bf16 between registers (row t / 4, columns 2 (t % 4) and
+// + 1) and shared memory, transposed; lane l gives row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- epilogue
 
 struct LinOut {
@@ -105,40 +138,148 @@ struct LinOut {
     long long ld;       // elements between consecutive c
 };
 
-// Columns [0, n) of one lane's accumulator row, n <= 32: output elements
-// (c0 + j, m). `at` = c0 * ld + m.
-template <LinMode MODE, int ACT>
-__device__ __forceinline__ void store_chunk(const LinOut &o, const float (&v)[32],
-                                            const uint16_t (&res)[32], float bias, long long at, int n)
+// A warp turns 32 m (its TMEM lanes) x 32 c of an accumulator into rows of out.
+// The accumulator has c along its columns and memory has m contiguous: pairs of
+// c are packed to bf16 in registers, stmatrix transposes them into 2 KB of the
+// warp's own shared memory, and each lane moves four 16-byte pieces (8 m of one
+// c) to memory; 1 store for 8 elements, where storing the columns one by one
+// took 22 instructions an element and held the gradient of 128 experts'
+// weights at 1.3 TB/s. The residual comes in the same way backwards, read by
+// the lane that will write it. Piece v of row c lies at v ^ (c / 2 % 4): no bank
+// conflict in either direction.
+constexpr int kStageBytes = 32 * 64;
+
+struct WarpStage {
+    uint32_t mat;       // shared address of this lane's row for ldmatrix / stmatrix, c group 0
+    uint4 *vec;         // this lane's piece of row lane / 4, c group 0
+    __device__ __forceinline__ WarpStage(uint8_t *base, int lane)
+    {
+        const int c = lane & 7, v = lane & 3;
+        mat = smem_u32(base) + c * 64 + (((lane >> 3) ^ (c >> 1)) & 3) * 16;
+        vec = reinterpret_cast<uint4 *>(base + (lane >> 2) * 64 + ((v ^ (lane >> 3)) & 3) * 16);
+    }
+};
+
+// The staged 32 x 32 values to dst + c * ld (dst: this lane's piece of row lane / 4).
+__device__ __forceinline__ void copy_out(const WarpStage &w, uint16_t *dst, long long ld8, int rows)
 {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (8 * i < rows)
+            *reinterpret_cast<uint4 *>(dst) = w.vec[i * 32];
+        dst += ld8;
+    }
+    __syncwarp();
+}
+
+// Columns [0, n) of the accumulator at taddr, n <= 32, to rows c0 + [0, n) of m
+// [m0, m0 + 32) cut at M. bias[i]: of m0 + 8 i + lane / 4. With `zero` the
+// accumulator holds nothing and the result is 0.
+template <LinMode MODE, int ACT>
+__device__ __forceinline__ void store_chunk(const LinOut &o, uint32_t taddr, bool zero,
+                                            const float (&bias)[4], long long c0, int m0, int M,
+                                            int n, int lane, const WarpStage &w)
+{
+    const int m = m0 + (lane & 3) * 8;
+    // rows this lane moves: c = lane / 4 + 8 i < n, none when its m lie past the end
+    const int rows = m < M ? n - (lane >> 2) : 0;
+    const long long at = (c0 + (lane >> 2)) * o.ld + m, ld8 = 8 * o.ld;
+    uint4 res[4];
+    if (MODE == LIN_FWD && o.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i < rows)
+                res[i] = *reinterpret_cast<const uint4 *>(o.residual + at + i * ld8);
+    }
+    float v[2][16];
+    if (zero) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[0][i] = v[1][i] = 0.f;
+    } else {
+        tmem_ld16(taddr, v[0]);
+        tmem_ld16(taddr + (16u << 16), v[1]);
+        tmem_ld_wait();
+    }
+    if (MODE == LIN_FWD) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i >> 4][i & 15] += bias[(i >> 4) * 2 + ((i >> 1) & 1)];
+        if (o.z) {
+#pragma unroll
+            for (int ci = 0; ci < 4; ++ci) {
+                uint32_t r[4];
+#pragma unroll
+                for (int mi = 0; mi < 4; ++mi) {
+                    const int k = 4 * ci + 2 * (mi & 1);
+                    r[mi] = pack_bf16x2(v[mi >> 1][k], v[mi >> 1][k + 1]);
+                }
+                stmatrix4_t(w.mat + ci * 512, r);
+            }
+            copy_out(w, o.z + at, ld8, rows);
+        }
+        if (o.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (8 * i < rows)
+                    w.vec[i * 32] = res[i];
+            __syncwarp();
+        }
+    }
+#pragma unroll
+    for (int ci = 0; ci < 4; ++ci) {
+        uint32_t r[4];
+        if (MODE == LIN_FWD && o.residual)
+            ldmatrix4_t(w.mat + ci * 512, r);
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi) {
+            const int k = 4 * ci + 2 * (mi & 1);
+            float a = act_f<ACT>(v[mi >> 1][k]), b = act_f<ACT>(v[mi >> 1][k + 1]);
+            if (MODE == LIN_FWD && o.residual) {
+                a += bf16lo(r[mi]);
+                b += bf16hi(r[mi]);
+            }
+            r[mi] = pack_bf16x2(a, b);
+        }
+        stmatrix4_t(w.mat + ci * 512, r);
+    }
+    copy_out(w, o.out + at, ld8, rows);
+}
+
+// The same for fp32 partial sums of dW: a lane holds one m of 32 columns, and a
+// warp's store is 128 contiguous bytes.
+__device__ __forceinline__ void store_part(float *part, long long ld, uint32_t taddr, bool zero,
+                                           long long c0, int m, int M, int n)
+{
+    float v[32];
+    if (zero) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = 0.f;
+    } else {
+        tmem_ld32(taddr, v);
+        tmem_ld_wait();
+    }
+    if (m >= M)
+        return;
+    float *dst = part + c0 * ld + m;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        if (j < n) {
-            const long long i = at + j * o.ld;
-            float f = v[j];
-            if (MODE == LIN_FWD) {
-                f += bias;
-                if (o.z)
-                    o.z[i] = (uint16_t)pack_bf16x2(f, 0.f);
-                f = act_f<ACT>(f);
-                if (o.residual)
-                    f += __uint_as_float((uint32_t)res[j] << 16);
-            }
-            if (MODE == LIN_DW && o.part)
-                o.part[i] = f;
-            else
-                o.out[i] = (uint16_t)pack_bf16x2(f, 0.f);
-        }
+        if (j < n)
+            *dst = v[j];
+        dst += ld;
     }
 }
 
 template <LinMode MODE>
-__device__ __forceinline__ void load_residual(const LinOut &o, uint16_t (&res)[32], long long at, int n)
+__device__ __forceinline__ void load_bias(const LinOut &o, long long first, int m0, int M, int lane,
+                                          float (&bias)[4])
 {
-    if (MODE == LIN_FWD && o.residual) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            res[j] = j < n ? o.residual[at + j * o.ld] : (uint16_t)0;
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + 8 * i + (lane >> 2);
+        bias[i] = (MODE == LIN_FWD && o.bias && m < M) ? o.bias[first + m] : 0.f;
     }
 }
 
@@ -154,7 +295,7 @@ constexpr int kPairThreads = 384;
 constexpr int kPairStages = 6;
 constexpr int kPairABytes = 2 * kBoxBytes;
 constexpr int kPairStage = 4 * kBoxBytes;   // A and B halves of one CTA
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + 8 * kStageBytes;
 
 struct PairArgs {
     const int32_t *offsets;
@@ -184,6 +325,17 @@ __device__ __forceinline__ int tile_rows(int n)
     return ((n + nt - 1) / nt + 31) & ~31;
 }
 
+// Tile of a pair in a round of npairs tiles. The turn by the golden ratio keeps a
+// pair from meeting one kind of tile only where tile_at mixes two.
+__device__ __forceinline__ int tile_of(int round, int pair, int npairs)
+{
+    const unsigned turn = __umulhi((unsigned)round * 2654435769u, (unsigned)npairs);
+    int at = pair + (int)turn;
+    if (at >= npairs)
+        at -= npairs;
+    return round * npairs + at;
+}
+
 template <LinMode MODE>
 __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G, int t)
 {
@@ -205,9 +357,18 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
         if (a.tail == kBox)
             a.tail = 0;
     } else {
-        const int it = t / p.m_tiles;
-        a.e = item_group(G, p.E, it);
-        const int f = G.first[a.e], ni = G.first[a.e + 1] - f;
+        // Groups of two or more items are bound by the tensor cores, those of one by
+        // reading their weights: the two are spread evenly over the tiles, so that
+        // they overlap.
+        const int big = G.first[G.nbig] * p.m_tiles, all = G.first[p.E] * p.m_tiles;
+        if (big > 0 && big < all) {
+            const int k = (int)((unsigned long long)t * big / all);
+            const int next = (int)((unsigned long long)(t + 1) * big / all);
+            t = next > k ? k : big + (t - k);
+        }
+        const int at = item_group(G, p.E, t / p.m_tiles);
+        a.e = G.group[at];
+        const int f = G.first[at], ni = G.first[at + 1] - f;
         const int local = t - f * p.m_tiles;
         const int per = p.band * p.m_tiles;
         const int b = local / per, r = local - b * per;
@@ -243,6 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint64_t *tailbar = tempty + 2;   // one a stage: several last blocks may be in flight
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tailbar + kPairStages);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint8_t *stage = smem + kPairStages * kPairStage + 256;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -271,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_trigger();
     // items of one group: token tiles; LIN_DW needs the groups' rows only
-    build_groups(G, p.offsets, p.E, p.rows, kTileC, p.status);
+    build_groups<true>(G, p.offsets, p.E, p.rows, kTileC, p.status);
     tc_fence_before();
     cluster_sync_all();   // both CTAs' barriers exist and TMEM is allocated
     tc_fence_after();
@@ -279,11 +441,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int total = MODE == LIN_DW ? p.E * p.splits * p.m_tiles * p.c_tiles
                                      : G.first[p.E] * p.m_tiles;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int rounds = (total + npairs - 1) / npairs;
 
     if (warp == 0) {
         if (lane == 0) {   // ---------------- producer (both CTAs)
             uint32_t it = 0;
-            for (int t = pair; t < total; t += npairs) {
+            for (int i = 0; i < rounds; ++i) {
+                const int t = tile_of(i, pair, npairs);
+                if (t >= total)
+                    break;
                 const TileAt a = tile_at<MODE>(p, G, t);
                 const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
                 const int nb = (half + kBox - 1) / kBox;
@@ -334,7 +500,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && leader) {   // ---------------- MMA issue
             uint32_t it = 0, local = 0;
-            for (int t = pair; t < total; t += npairs) {
+            for (int i = 0; i < rounds; ++i) {
+                const int t = tile_of(i, pair, npairs);
+                if (t >= total)
+                    break;
                 const TileAt a = tile_at<MODE>(p, G, t);
                 if (MODE == LIN_DW && a.nkb == 0)
                     continue;            // nothing to add up: the epilogue writes zeros
@@ -362,8 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t a0 = smem_u32(smem + s * kPairStage), b0 = a0 + kPairABytes;
 #pragma unroll
                     for (int kk = 0; kk < kBox / 16; ++kk)
-                        tc_mma_bf16_pair(d, op_desc<A_MN>(a0, kk), op_desc<B_MN>(b0, kk), idesc,
-                                         (kb | kk) != 0);
+                        if (!tail || kk * 16 < a.tail)
+                            tc_mma_bf16_pair(d, op_desc<A_MN>(a0, kk), op_desc<B_MN>(b0, kk), idesc,
+                                             (kb | kk) != 0);
                     tc_commit_pair(&empty[s], 0x3);
                 }
                 if (!ok)
@@ -373,7 +543,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else if (MODE == LIN_DW && warp == 2) {   // ---------------- last blocks (both CTAs)
         uint32_t it = 0, phases = 0;   // bit s: parity of stage s's next use
-        for (int t = pair; t < total; t += npairs) {
+        for (int i = 0; i < rounds; ++i) {
+            const int t = tile_of(i, pair, npairs);
+            if (t >= total)
+                break;
             const TileAt a = tile_at<MODE>(p, G, t);
             it += a.nkb;
             if (!a.tail)
@@ -383,13 +556,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 break;
             phases ^= 1u << s;
             // row r of a 64 x 64 box is its bytes [128 r, 128 r + 128): the swizzle
-            // only permutes the 16-byte pieces of a row
-            const int per = (kBox - a.tail) * 8;
-            const int nb = (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
-            uint8_t *sa = smem + s * kPairStage;
-            for (int i = lane; i < (2 + nb) * per; i += 32)
-                reinterpret_cast<uint4 *>(sa + (i / per) * kBoxBytes + a.tail * 128)[i % per] =
-                    make_uint4(0, 0, 0, 0);
+            // only permutes the 16-byte pieces of a row. Rows past the last K step of
+            // 16 that the MMAs take need no zeros.
+            const int end = (a.tail + 15) & ~15;
+            const int boxes = 2 + (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
+            for (int r = a.tail + (lane >> 3); r < end; r += 4)
+                for (int j = 0; j < boxes; ++j)
+                    *reinterpret_cast<uint4 *>(smem + s * kPairStage + j * kBoxBytes + r * 128 +
+                                               (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0)
@@ -398,19 +572,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp >= 4) {   // ---------------- epilogue (both CTAs)
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
+        const WarpStage ws(stage + (warp - 4) * kStageBytes, lane);
         uint32_t local = 0;
-        for (int t = pair; t < total; t += npairs) {
+        for (int i = 0; i < rounds; ++i) {
+            const int t = tile_of(i, pair, npairs);
+            if (t >= total)
+                break;
             const TileAt a = tile_at<MODE>(p, G, t);
-            const int m = a.m0 + 128 * (int)rank + q * 32 + lane;
-            const bool ok = m < M;
-            const long long base =
-                MODE == LIN_DW ? ((long long)(p.o.part ? a.split * p.E : 0) + a.e) * p.d_out * p.o.ld
-                               : 0;
+            const int m0 = a.m0 + 128 * (int)rank + q * 32;
+            // first row of the output: dW's rows count from expert (and split) 0
+            const long long c00 =
+                MODE == LIN_DW ? ((long long)(p.o.part ? a.split * p.E : 0) + a.e) * p.d_out : 0;
             const bool none = MODE == LIN_DW && a.nkb == 0;
             const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
-            float bias = 0.f;
-            if (MODE == LIN_FWD && p.o.bias && ok)
-                bias = p.o.bias[(long long)a.e * p.d_out + m];
+            float bias[4];
+            load_bias<MODE>(p.o, (long long)a.e * p.d_out, m0, M, lane, bias);
             if (!none) {
                 if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
                     break;
@@ -418,25 +594,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 tc_fence_after();
             }
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kTileC;
+            if (m0 < M) {
 #pragma unroll 1
-            for (int c = h * 32; c < a.cn; c += 64) {
-                const int n = min(32, a.cn - c);
-                const long long at = base + (long long)(a.c0 + c) * p.o.ld + m;
-                float v[32];
-                uint16_t res[32];
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = 0.f;
-                } else {
-                    tmem_ld32(tb + c, v);
+                for (int c = h * 32; c < a.cn; c += 64) {
+                    const int n = min(32, a.cn - c);
+                    if (MODE == LIN_DW && p.o.part)
+                        store_part(p.o.part, p.o.ld, tb + c, none, c00 + a.c0 + c, m0 + lane, M, n);
+                    else
+                        store_chunk<MODE, ACT>(p.o, tb + c, none, bias, c00 + a.c0 + c, m0, M, n,
+                                               lane, ws);
                 }
-                if (ok)
-                    load_residual<MODE>(p.o, res, at, n);
-                if (!none)
-                    tmem_ld_wait();
-                if (ok)
-                    store_chunk<MODE, ACT>(p.o, v, res, bias, at, n);
             }
             if (!none) {
                 tc_fence_before();
@@ -585,20 +752,16 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
     const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     if (p.S == 1) {
-        const int m = m0 + q * 32 + lane;
-        const float bias = (MODE == LIN_FWD && p.o.bias && m < M) ? p.o.bias[(long long)e * p.d_out + m] : 0.f;
+        // the ring, which every copy and MMA has left, holds the rows on their way out
+        const WarpStage ws(smem + warp * kStageBytes, lane);
+        const int mq = m0 + q * 32;
+        float bias[4];
+        load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
+        if (got && mq < M) {
 #pragma unroll 1
-        for (int c = h * 32; got && c < cn; c += 64) {
-            const int n = min(32, cn - c);
-            const long long at = (long long)(c0 + c) * p.o.ld + m;
-            float v[32];
-            uint16_t res[32];
-            tmem_ld32(tb + c, v);
-            if (m < M)
-                load_residual<MODE>(p.o, res, at, n);
-            tmem_ld_wait();
-            if (m < M)
-                store_chunk<MODE, ACT>(p.o, v, res, bias, at, n);
+            for (int c = h * 32; c < cn; c += 64)
+                store_chunk<MODE, ACT>(p.o, tb + c, false, bias, c0 + c, mq, M, min(32, cn - c), lane,
+                                       ws);
         }
     } else {
         // partial sums [c][128 m] over the ring, which every copy and MMA has left

@@ -197,7 +197,8 @@ def _host_ptr(t, dtype, name):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: current_stream() builds an object for it, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -397,13 +398,39 @@ def _on_one_device(**tensors):
         raise ValueError("tensors on different devices: " + ", ".join(
             f"{n} on {t.device}" for n, t in tensors.items()
             if isinstance(t, torch.Tensor) and t.is_cuda))
-    return torch.cuda.device(devs.pop()) if devs else contextlib.nullcontext()
+    return torch.cuda.device(devs.pop()) if devs else _HERE
 
 
-def _has(t, shape, name):
-    if t is not None and isinstance(t, torch.Tensor) and tuple(t.shape) not in (
-            tuple(shape), tuple(shape[1:]) if shape[0] == 1 else tuple(shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+_HERE = contextlib.nullcontext()
+
+
+def _args(*specs):
+    """Checked pointers of tensors given as (tensor, dtype or None, shape or None, name), and the
+    context of _on_one_device. An expected leading axis of 1 may be missing."""
+    ptrs, here = [], -1
+    for t, dtype, shape, name in specs:   # what nearly every call passes, with few steps
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and
+                (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
+            break
+        if here < 0:
+            here = torch.cuda.current_device()
+        if t.get_device() != here:
+            break
+        ptrs.append(t.data_ptr())
+    else:
+        return ptrs, _HERE
+    for t, _, shape, name in specs:
+        if shape is not None and isinstance(t, torch.Tensor) and t.shape != shape and (
+                shape[0] != 1 or t.shape != shape[1:]):
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    ptrs, named = [], {}
+    for i, (t, dtype, _, name) in enumerate(specs):
+        ptrs.append(_ptr(t, dtype, name))
+        named[f"{name}[{i}]" if name in named else name] = t
+    return ptrs, _on_one_device(**named)
 
 
 def _at_least(t, n, name):
@@ -428,52 +455,45 @@ def moe_linear_forward(shape, x, expert_offsets, W, bias, residual, y, z=None, s
     """y = act(x W_e^T + b_e) + residual over the groups of expert_offsets (None: dense, E = 1);
     z (optional) receives the pre-activation. With E = 1, W and bias may lack the expert axis."""
     R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
-    for t, shp, name in ((x, (R, di), "x"), (W, (E, do, di), "W"), (bias, (E, do), "bias"),
-                         (residual, (R, do), "residual"), (y, (R, do), "y"), (z, (R, do), "z")):
-        _has(t, shp, name)
     _at_least(expert_offsets, E + 1, "expert_offsets")
     _at_least(status, 1, "status")
-    with _on_one_device(x=x, expert_offsets=expert_offsets, W=W, bias=bias, residual=residual, y=y,
-                        z=z, status=status):
-        _check("moe_linear_forward", lib().moe_linear_forward(
-            ctypes.byref(shape), _ptr(x, BF16, "x"), _ptr(expert_offsets, I32, "expert_offsets"),
-            _ptr(W, BF16, "W"), _ptr(bias, F32, "bias"), _ptr(residual, BF16, "residual"),
-            _ptr(y, BF16, "y"), _ptr(z, BF16, "z"), _ptr(status, U32, "status"), _stream(stream)))
+    ptrs, on_device = _args(
+        (x, BF16, (R, di), "x"), (expert_offsets, I32, None, "expert_offsets"),
+        (W, BF16, (E, do, di), "W"), (bias, F32, (E, do), "bias"),
+        (residual, BF16, (R, do), "residual"), (y, BF16, (R, do), "y"), (z, BF16, (R, do), "z"),
+        (status, U32, None, "status"))
+    with on_device:
+        _check("moe_linear_forward",
+               lib().moe_linear_forward(ctypes.byref(shape), *ptrs, _stream(stream)))
     return y
 
 
 def moe_linear_backward(shape, x, expert_offsets, W, z, dy, dx, dW, dbias, status, ws, stream=None):
     """Gradients of sum(y * dy): dx, dW and dbias (each may be None)."""
     R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
-    for t, shp, name in ((x, (R, di), "x"), (W, (E, do, di), "W"), (z, (R, do), "z"),
-                         (dy, (R, do), "dy"), (dx, (R, di), "dx"), (dW, (E, do, di), "dW"),
-                         (dbias, (E, do), "dbias")):
-        _has(t, shp, name)
     _at_least(expert_offsets, E + 1, "expert_offsets")
     _at_least(status, 1, "status")
-    with _on_one_device(x=x, expert_offsets=expert_offsets, W=W, z=z, dy=dy, dx=dx, dW=dW,
-                        dbias=dbias, status=status, ws=ws):
+    ptrs, on_device = _args(
+        (x, BF16, (R, di), "x"), (expert_offsets, I32, None, "expert_offsets"),
+        (W, BF16, (E, do, di), "W"), (z, BF16, (R, do), "z"), (dy, BF16, (R, do), "dy"),
+        (dx, BF16, (R, di), "dx"), (dW, BF16, (E, do, di), "dW"), (dbias, F32, (E, do), "dbias"),
+        (status, U32, None, "status"), (ws, None, None, "ws"))
+    with on_device:
         _check("moe_linear_backward", lib().moe_linear_backward(
-            ctypes.byref(shape), _ptr(x, BF16, "x"), _ptr(expert_offsets, I32, "expert_offsets"),
-            _ptr(W, BF16, "W"), _ptr(z, BF16, "z"), _ptr(dy, BF16, "dy"), _ptr(dx, BF16, "dx"),
-            _ptr(dW, BF16, "dW"), _ptr(dbias, F32, "dbias"), _ptr(status, U32, "status"),
-            _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+            ctypes.byref(shape), *ptrs, _nbytes(ws), _stream(stream)))
 
 
 def moe_combine_rows(shape, y_perm, slot_pos, topk_w, residual, out, status=None, stream=None):
     """out[t] = residual[t] + sum_j w[t,j] y_perm[slot_pos[t,j]], bf16 rows (topk_w None: all 1)."""
     T, d, k = shape.T, shape.d, shape.k
-    for t, shp, name in ((y_perm, (T * k, d), "y_perm"), (slot_pos, (T, k), "slot_pos"),
-                         (topk_w, (T, k), "topk_w"), (residual, (T, d), "residual"),
-                         (out, (T, d), "out")):
-        _has(t, shp, name)
     _at_least(status, 1, "status")
-    with _on_one_device(y_perm=y_perm, slot_pos=slot_pos, topk_w=topk_w, residual=residual, out=out,
-                        status=status):
-        _check("moe_combine_rows", lib().moe_combine_rows(
-            ctypes.byref(shape), _ptr(y_perm, BF16, "y_perm"), _ptr(slot_pos, I32, "slot_pos"),
-            _ptr(topk_w, F32, "topk_w"), _ptr(residual, BF16, "residual"), _ptr(out, BF16, "out"),
-            _ptr(status, U32, "status"), _stream(stream)))
+    ptrs, on_device = _args(
+        (y_perm, BF16, (T * k, d), "y_perm"), (slot_pos, I32, (T, k), "slot_pos"),
+        (topk_w, F32, (T, k), "topk_w"), (residual, BF16, (T, d), "residual"),
+        (out, BF16, (T, d), "out"), (status, U32, None, "status"))
+    with on_device:
+        _check("moe_combine_rows",
+               lib().moe_combine_rows(ctypes.byref(shape), *ptrs, _stream(stream)))
     return out
 
 
@@ -481,31 +501,33 @@ def moe_combine_rows_backward(shape, dout, y_perm, slot_pos, topk_w, dy_perm, dt
                               stream=None):
     """Gradients of sum(out * dout) of moe_combine_rows: dy_perm and dtopk_w (either may be None)."""
     T, d, k = shape.T, shape.d, shape.k
-    for t, shp, name in ((dout, (T, d), "dout"), (y_perm, (T * k, d), "y_perm"),
-                         (slot_pos, (T, k), "slot_pos"), (topk_w, (T, k), "topk_w"),
-                         (dy_perm, (T * k, d), "dy_perm"), (dtopk_w, (T, k), "dtopk_w")):
-        _has(t, shp, name)
     _at_least(status, 1, "status")
-    with _on_one_device(dout=dout, y_perm=y_perm, slot_pos=slot_pos, topk_w=topk_w, dy_perm=dy_perm,
-                        dtopk_w=dtopk_w, status=status):
-        _check("moe_combine_rows_backward", lib().moe_combine_rows_backward(
-            ctypes.byref(shape), _ptr(dout, BF16, "dout"), _ptr(y_perm, BF16, "y_perm"),
-            _ptr(slot_pos, I32, "slot_pos"), _ptr(topk_w, F32, "topk_w"),
-            _ptr(dy_perm, BF16, "dy_perm"), _ptr(dtopk_w, F32, "dtopk_w"),
-            _ptr(status, U32, "status"), _stream(stream)))
+    ptrs, on_device = _args(
+        (dout, BF16, (T, d), "dout"), (y_perm, BF16, (T * k, d), "y_perm"),
+        (slot_pos, I32, (T, k), "slot_pos"), (topk_w, F32, (T, k), "topk_w"),
+        (dy_perm, BF16, (T * k, d), "dy_perm"), (dtopk_w, F32, (T, k), "dtopk_w"),
+        (status, U32, None, "status"))
+    with on_device:
+        _check("moe_combine_rows_backward",
+               lib().moe_combine_rows_backward(ctypes.byref(shape), *ptrs, _stream(stream)))
+
+
+_KINDS = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
 
 
 def _tensor_list(tensors, name):
-    """(pointers, element counts, MOE_TYPE_*) of fp32 / bf16 tensors, as host arrays."""
-    kinds = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
+    """(pointers, element counts, MOE_TYPE_*) of fp32 / bf16 tensors on one device, as host
+    arrays."""
+    ptrs, _ = _args(*((t, None, None, name) for t in tensors))
     n = len(tensors)
-    ptrs, numel, types = (_P * max(n, 1))(), (ctypes.c_int64 * max(n, 1))(), (ctypes.c_int32 * max(n, 1))()
+    types = []
     for i, t in enumerate(tensors):
-        p = _ptr(t, None, f"{name}[{i}]")
-        if t.dtype not in kinds:
-            raise TypeError(f"{name}[{i}]: expected float32 or bfloat16, got {t.dtype}")
-        ptrs[i], numel[i], types[i] = p, t.numel(), kinds[t.dtype]
-    return ptrs, numel, types
+        if t is None or t.dtype not in _KINDS:
+            raise TypeError(f"{name}[{i}]: expected float32 or bfloat16, got "
+                            f"{None if t is None else t.dtype}")
+        types.append(_KINDS[t.dtype])
+    return ((_P * n)(*ptrs), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int32 * n)(*types))
 
 
 def alloc_grad_workspace(grads=(), device="cuda") -> torch.Tensor:
@@ -520,11 +542,12 @@ def moe_grad_norm(grads, norm, status=None, ws=None, stream=None):
     ptrs, numel, types = _tensor_list(grads, "grads")
     _at_least(norm, 1, "norm")
     _at_least(status, 1, "status")
-    with _on_one_device(norm=norm, status=status, ws=ws,
-                        **{f"grads[{i}]": t for i, t in enumerate(grads)}):
+    (norm_p, status_p, ws_p, *_), on_device = _args(
+        (norm, F32, None, "norm"), (status, U32, None, "status"), (ws, None, None, "ws"),
+        *((t, None, None, "grads") for t in grads[:1]))
+    with on_device:
         _check("moe_grad_norm", lib().moe_grad_norm(
-            len(grads), ptrs, numel, types, _ptr(norm, F32, "norm"), _ptr(status, U32, "status"),
-            _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+            len(grads), ptrs, numel, types, norm_p, status_p, ws_p, _nbytes(ws), _stream(stream)))
     return norm
 
 
@@ -533,8 +556,7 @@ def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, strea
     in place, or into `outs`."""
     grads = list(grads)
     ptrs, numel, types = _tensor_list(grads, "grads")
-    optrs = None
-    named = {f"grads[{i}]": t for i, t in enumerate(grads)}
+    optrs, firsts = None, grads[:1]
     if outs is not None:
         outs = list(outs)
         if len(outs) != len(grads):
@@ -542,14 +564,17 @@ def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, strea
         for i, (g, o) in enumerate(zip(grads, outs)):
             if g.dtype != o.dtype or g.numel() != o.numel():
                 raise ValueError(f"outs[{i}]: must match grads[{i}] in type and size")
-        optrs, _, _ = _tensor_list(outs, "outs")
-        named |= {f"outs[{i}]": t for i, t in enumerate(outs)}
+        optrs = _tensor_list(outs, "outs")[0]
+        firsts = firsts + outs[:1]
     _at_least(norm, 1, "norm")
     _at_least(status, 1, "status")
-    with _on_one_device(norm=norm, status=status, ws=ws, **named):
+    (norm_p, status_p, ws_p, *_), on_device = _args(
+        (norm, F32, None, "norm"), (status, U32, None, "status"), (ws, None, None, "ws"),
+        *((t, None, None, "grads / outs") for t in firsts))
+    with on_device:
         _check("moe_clip_grads", lib().moe_clip_grads(
-            len(grads), ptrs, optrs, numel, types, float(max_norm), _ptr(norm, F32, "norm"),
-            _ptr(status, U32, "status"), _ptr(ws, name="ws"), _nbytes(ws), _stream(stream)))
+            len(grads), ptrs, optrs, numel, types, float(max_norm), norm_p, status_p, ws_p,
+            _nbytes(ws), _stream(stream)))
     return norm
 
 
