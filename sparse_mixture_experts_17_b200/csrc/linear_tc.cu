@@ -51,6 +51,15 @@ __device__ __forceinline__ void tma_3d(void *dst, const void *tmap, int c0, int 
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3,
+                                       uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                 "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_3d_pair(void *dst, const void *tmap, int c0, int c1, int c2,
                                             uint32_t bar_cluster)
 {
@@ -58,6 +67,16 @@ __device__ __forceinline__ void tma_3d_pair(void *dst, const void *tmap, int c0,
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_4d_pair(void *dst, const void *tmap, int c0, int c1, int c2,
+                                            int c3, uint32_t bar_cluster)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar_cluster)
         : "memory");
 }
 
@@ -305,8 +324,18 @@ struct PairArgs {
     int kblocks;     // LIN_FWD, LIN_DX
     int band;        // items of a group whose B rows stay in L2 while W passes by
     int splits;      // LIN_DW
+    bool a_wide, b_wide;   // MN-major operands: two boxes in one copy
     LinOut o;
     uint32_t *status;
+};
+
+// Maps of the tokens' operand with boxes of 16, 32, 64 and 128 rows: a tile takes
+// its rows in one copy that is no larger than it has to be. (LIN_DW: box[0] only.)
+// Copies are issued by one thread, and their number counts as well as their
+// bytes: with two boxes of 64 rows in place of one of 128 the loads alone of
+// 16384 x 14336 -> 4096 took 1100 us, with one 835.
+struct BMaps {
+    CUtensorMap box[4];
 };
 
 struct TileAt {
@@ -389,7 +418,7 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
 
 template <LinMode MODE, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
                   const PairArgs p)
 {
     constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
@@ -424,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmB.box[MODE == LIN_DW ? 0 : 3]);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -452,9 +481,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     break;
                 const TileAt a = tile_at<MODE>(p, G, t);
                 const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
-                const int nb = (half + kBox - 1) / kBox;
                 const int c0 = a.c0 + (int)rank * half, m0 = a.m0 + 128 * (int)rank;
-                const uint32_t bytes = kPairABytes + nb * kBoxBytes;
+                const int fit = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+                const int nb = p.b_wide ? 1 : (half + kBox - 1) / kBox;   // LIN_DW: copies of B
+                const uint32_t bytes =
+                    kPairABytes + (MODE == LIN_DW ? (p.b_wide ? 2 : nb) * kBoxBytes : 2048 << fit);
                 bool ok = true;
                 for (int kb = 0; kb < a.nkb; ++kb, ++it) {
                     const int s = it % kPairStages;
@@ -479,18 +510,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const int k = kb * kBox;
                     if (MODE == LIN_FWD) {
                         tma_3d_pair(sa, &tmA, k, m0, a.e, bar);
-                    } else if (MODE == LIN_DX) {
-                        tma_3d_pair(sa, &tmA, m0, k, a.e, bar);
-                        tma_3d_pair(sa + kBoxBytes, &tmA, m0 + kBox, k, a.e, bar);
-                    } else {
-                        tma_load_2d_pair(sa, &tmA, m0, a.r0 + k, bar);
-                        tma_load_2d_pair(sa + kBoxBytes, &tmA, m0 + kBox, a.r0 + k, bar);
+                        tma_load_2d_pair(sb, &tmB.box[fit], k, c0, bar);
+                        continue;
                     }
-                    for (int j = 0; j < nb; ++j) {
-                        if (MODE == LIN_DW)
-                            tma_load_2d_pair(sb + j * kBoxBytes, &tmB, c0 + j * kBox, a.r0 + k, bar);
-                        else
-                            tma_load_2d_pair(sb + j * kBoxBytes, &tmB, k, c0 + j * kBox, bar);
+                    const int ka = MODE == LIN_DX ? k : a.r0 + k, ea = MODE == LIN_DX ? a.e : 0;
+                    if (p.a_wide) {
+                        tma_4d_pair(sa, &tmA, 0, ka, m0 / kBox, ea, bar);
+                    } else {
+                        tma_4d_pair(sa, &tmA, m0, ka, 0, ea, bar);
+                        tma_4d_pair(sa + kBoxBytes, &tmA, m0 + kBox, ka, 0, ea, bar);
+                    }
+                    if (MODE == LIN_DX) {
+                        tma_load_2d_pair(sb, &tmB.box[fit], k, c0, bar);
+                    } else if (p.b_wide) {
+                        tma_4d_pair(sb, &tmB.box[0], 0, ka, c0 / kBox, 0, bar);
+                    } else {
+                        for (int j = 0; j < nb; ++j)
+                            tma_4d_pair(sb + j * kBoxBytes, &tmB.box[0], c0 + j * kBox, ka, 0, 0, bar);
                     }
                 }
                 if (!ok)
@@ -559,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // only permutes the 16-byte pieces of a row. Rows past the last K step of
             // 16 that the MMAs take need no zeros.
             const int end = (a.tail + 15) & ~15;
-            const int boxes = 2 + (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
+            const int boxes = p.b_wide ? 4 : 2 + (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
             for (int r = a.tail + (lane >> 3); r < end; r += 4)
                 for (int j = 0; j < boxes; ++j)
                     *reinterpret_cast<uint4 *>(smem + s * kPairStage + j * kBoxBytes + r * 128 +
@@ -636,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // start and end hide behind the other's loads.
 template <int BC>
 struct SplitCfg {
-    static constexpr int BOXROWS = BC < 64 ? BC : 64;
+    static constexpr int BOXROWS = BC < 128 ? BC : 128;
     static constexpr int A_BYTES = 2 * kBoxBytes;
     static constexpr int B_BYTES = BC * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -650,6 +686,7 @@ struct SplitArgs {
     int E, rows, d_in, d_out;
     int S;
     int kblocks;
+    bool a_wide;
     LinOut o;
     uint32_t *status;
 };
@@ -714,9 +751,11 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
             uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
             mbar_arrive_expect_tx(&full[s], bytes);
             const int k = (k0 + i) * kBox;
-            if (A_MN) {
-                tma_3d(sa, &tmA, m0, k, e, &full[s]);
-                tma_3d(sa + kBoxBytes, &tmA, m0 + kBox, k, e, &full[s]);
+            if (A_MN && p.a_wide) {
+                tma_4d(sa, &tmA, 0, k, m0 / kBox, e, &full[s]);
+            } else if (A_MN) {
+                tma_4d(sa, &tmA, m0, k, 0, e, &full[s]);
+                tma_4d(sa + kBoxBytes, &tmA, m0 + kBox, k, 0, e, &full[s]);
             } else {
                 tma_3d(sa, &tmA, k, m0, e, &full[s]);
             }
@@ -867,23 +906,42 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
+int encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
+           const cuuint64_t *strides, const cuuint32_t *box)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return MOE_ERR_CUDA;
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // bf16 [depth, rows, cols] (depth 0: two-dimensional); boxes of 64 x box_rows
 // elements, 128-byte swizzle, zero fill outside.
 int make_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long depth,
              int box_rows)
 {
-    auto fn = encode_fn();
-    if (!fn)
-        return MOE_ERR_CUDA;
-    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-    cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
-    cuuint32_t box[3] = {(cuuint32_t)kBox, (cuuint32_t)box_rows, 1u};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth ? 3 : 2,
-                          const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kBox, (cuuint32_t)box_rows, 1u};
+    return encode(m, base, depth ? 3 : 2, dims, strides, box);
+}
+
+// The same matrices for an MN-major operand, boxes of 64 x 64. `wide` (cols a
+// multiple of 64): as [depth, cols / 64, rows, 64], two neighbouring boxes in one copy.
+int make_map_mn(CUtensorMap *m, const void *base, long long cols, long long rows, long long depth,
+                bool wide)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)(wide ? kBox : cols), (cuuint64_t)rows,
+                                (cuuint64_t)(wide ? cols / kBox : 1), (cuuint64_t)depth};
+    const cuuint64_t strides[3] = {(cuuint64_t)cols * 2, (cuuint64_t)kBox * 2,
+                                   (cuuint64_t)cols * rows * 2};
+    const cuuint32_t box[4] = {(cuuint32_t)kBox, (cuuint32_t)kBox, wide ? 2u : 1u, 1u};
+    return encode(m, base, 4, dims, strides, box);
 }
 
 template <class K>
@@ -910,23 +968,30 @@ LinOut out_of(LinMode mode, const LinArgs &a)
     return o;
 }
 
-// Maps of the two operands. A: W [E, d_out, d_in] (box 128 rows when K-major, 64
-// when MN-major), or x for dW. B: the rows of x or dz.
-int operand_maps(LinMode mode, const LinArgs &a, int b_box_rows, CUtensorMap *A, CUtensorMap *B)
+// Map of the tokens' operand (LIN_FWD, LIN_DX) with boxes of box_rows rows.
+int token_map(LinMode mode, const LinArgs &a, int box_rows, CUtensorMap *B)
 {
-    int rc = mode == LIN_DW ? make_map(A, a.x, a.d_in, a.rows, 0, kBox)
-                            : make_map(A, a.W, a.d_in, a.d_out, a.E, mode == LIN_FWD ? 128 : kBox);
-    if (rc)
-        return rc;
-    return mode == LIN_FWD ? make_map(B, a.x, a.d_in, a.rows, 0, b_box_rows)
-                           : make_map(B, a.dz, a.d_out, a.rows, 0, b_box_rows);
+    return mode == LIN_FWD ? make_map(B, a.x, a.d_in, a.rows, 0, box_rows)
+                           : make_map(B, a.dz, a.d_out, a.rows, 0, box_rows);
 }
 
 template <LinMode MODE, int ACT>
 int launch_pair(const LinArgs &a, cudaStream_t st)
 {
-    CUtensorMap A, B;
-    int rc = operand_maps(MODE, a, kBox, &A, &B);
+    CUtensorMap A;
+    BMaps B;
+    // a tile's m start at multiples of 128; its two halves of c at multiples of 64
+    // where all c come in multiples of 128
+    const bool a_wide = a.d_in % kBox == 0, b_wide = MODE == LIN_DW && a.d_out % 128 == 0;
+    int rc;
+    if (MODE == LIN_FWD)
+        rc = make_map(&A, a.W, a.d_in, a.d_out, a.E, 128);
+    else if (MODE == LIN_DX)
+        rc = make_map_mn(&A, a.W, a.d_in, a.d_out, a.E, a_wide);
+    else if (!(rc = make_map_mn(&A, a.x, a.d_in, a.rows, 1, a_wide)))
+        rc = make_map_mn(&B.box[0], a.dz, a.d_out, a.rows, 1, b_wide);
+    for (int i = 0; i < 4 && !rc && MODE != LIN_DW; ++i)
+        rc = token_map(MODE, a, 16 << i, &B.box[i]);
     if (rc || (rc = allow_smem(k_linear_pair<MODE, ACT>, kPairSmem)))
         return rc;
     PairArgs p;
@@ -943,6 +1008,8 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
     // a band's token rows stay in L2 (48 MiB of them) while it sweeps the m tiles
     p.band = (int)std::max<long long>((48LL << 20) / ((long long)kTileC * K * 2), 1);
     p.splits = std::max(a.splits, 1);
+    p.a_wide = a_wide;
+    p.b_wide = b_wide;
     p.o = out_of(MODE, a);
     p.status = a.status;
     const long long tiles =
@@ -967,8 +1034,11 @@ int launch_split(const LinArgs &a, int S, cudaStream_t st)
 {
     using C = SplitCfg<BC>;
     CUtensorMap A, B;
-    int rc = operand_maps(MODE, a, C::BOXROWS, &A, &B);
-    if (rc || (rc = allow_smem(k_linear_split<MODE, ACT, BC>, C::SMEM)))
+    const bool a_wide = a.d_in % kBox == 0;
+    int rc = MODE == LIN_FWD ? make_map(&A, a.W, a.d_in, a.d_out, a.E, 128)
+                             : make_map_mn(&A, a.W, a.d_in, a.d_out, a.E, a_wide);
+    if (rc || (rc = token_map(MODE, a, C::BOXROWS, &B)) ||
+        (rc = allow_smem(k_linear_split<MODE, ACT, BC>, C::SMEM)))
         return rc;
     SplitArgs p;
     std::memset(&p, 0, sizeof p);
@@ -978,6 +1048,7 @@ int launch_split(const LinArgs &a, int S, cudaStream_t st)
     p.d_in = a.d_in;
     p.d_out = a.d_out;
     p.S = S;
+    p.a_wide = a_wide;
     p.kblocks = ceil_div(MODE == LIN_FWD ? a.d_in : a.d_out, kBox);
     p.o = out_of(MODE, a);
     p.status = a.status;
