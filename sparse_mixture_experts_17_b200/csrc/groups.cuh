@@ -14,17 +14,20 @@ namespace moe {
 struct GroupSmem {
     int row0[MOE_MAX_E + 1];    // first row of each group, so [e + 1] is the end of group e
     int first[MOE_MAX_E + 1];   // first item of each group; [E]: number of items
-    int group[MOE_MAX_E];       // ORDER: the groups' places in first[]
-    int nbig;                   // ORDER: groups of two or more items, which come first
+    int group[MOE_MAX_E];       // ORDER: the group at each place of first[]
+    int cls[4];                 // ORDER: first item of each class, and the end of the last
     unsigned long long warp[8];
     int bad;
 };
 
 // Fills G. All threads of a block of >= 256 threads (a multiple of 32) call it;
 // the first 256 work. offsets NULL: one group of all rows. Offsets that decrease
-// or leave [0, rows] make every group empty and flag MOE_ERR_CHECK. With ORDER,
-// first[] runs over the groups of two or more items and then over the others,
-// and group[i] is the group at place i (row0 stays by group).
+// or leave [0, rows] make every group empty and flag MOE_ERR_CHECK. With ORDER
+// (item_rows >= kClass1Rows), first[] runs over the groups by class, and group[i] is the
+// group at place i (row0 stays by group): class 0 has more than kClass1Rows rows,
+// class 1 more than kClass2Rows, class 2 at least one; empty groups come last.
+constexpr int kClass1Rows = 128, kClass2Rows = 64;
+
 template <bool ORDER = false>
 __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offsets, int E, int rows,
                                              int item_rows, uint32_t *status)
@@ -48,11 +51,12 @@ __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offset
             flag_status(status, MOE_ERR_CHECK);
     }
     const int n = (b - a + item_rows - 1) / item_rows;
-    // exclusive scan over the first 256 threads of the items (26 bits: at most 2^24 + 256),
-    // and with ORDER also of the big groups' items and of the big groups themselves (9 bits)
-    const bool big = ORDER && n > 1 && t < E;
-    const unsigned long long mine = (unsigned long long)n | (big ? (unsigned long long)n << 26 : 0) |
-                                    (big ? 1ull << 52 : 0);
+    // exclusive scan over the first 256 threads: the items (26 bits: at most 2^24 + 256), with
+    // ORDER those of class 0 only, and the groups of each class (9 bits each)
+    const int c = b - a > kClass1Rows ? 0 : b - a > kClass2Rows ? 1 : 2;
+    unsigned long long mine = (unsigned long long)n;
+    if (ORDER)
+        mine = n == 0 ? 0 : c == 0 ? mine | 1ull << 26 : 1ull << (26 + 9 * c);
     const int lane = t & 31, warp = t >> 5;
     unsigned long long inc = mine;
 #pragma unroll
@@ -73,20 +77,38 @@ __device__ __forceinline__ void build_groups(GroupSmem &G, const int32_t *offset
         }
         const unsigned long long ex = base + inc - mine;
         const int mask = (1 << 26) - 1;
-        const int all = (int)(ex & mask), in_big = (int)(ex >> 26) & mask, bigs = (int)(ex >> 52);
+        const int items = (int)(ex & mask), all = (int)(sum & mask);
         if (ORDER) {
-            const int nbig = (int)(sum >> 52), big_items = (int)(sum >> 26) & mask;
-            const int place = big ? bigs : nbig + t - bigs;
-            G.first[place] = big ? in_big : big_items + all - in_big;
+            const auto part = [](unsigned long long v, int c) { return (int)(v >> (26 + 9 * c)) & 511; };
+            const int r0 = part(ex, 0), r1 = part(ex, 1), r2 = part(ex, 2);
+            const int n0 = part(sum, 0), n1 = part(sum, 1), n2 = part(sum, 2);
+            const int end1 = all + n1, end2 = end1 + n2;
+            int place, first;
+            if (n == 0) {
+                place = n0 + n1 + n2 + t - r0 - r1 - r2;
+                first = end2;
+            } else if (c == 0) {
+                place = r0;
+                first = items;
+            } else if (c == 1) {
+                place = n0 + r1;
+                first = all + r1;
+            } else {
+                place = n0 + n1 + r2;
+                first = end1 + r2;
+            }
+            G.first[place] = first;
             G.group[place] = t;
             if (t == 0) {
-                G.nbig = nbig;
-                G.first[E] = (int)(sum & mask);
+                G.cls[0] = 0;
+                G.cls[1] = all;
+                G.cls[2] = end1;
+                G.cls[3] = G.first[E] = end2;
             }
         } else {
-            G.first[t] = all;
+            G.first[t] = items;
             if (t == 0)
-                G.first[E] = (int)(sum & mask);
+                G.first[E] = all;
         }
         G.row0[t] = a;
         if (t == E - 1)

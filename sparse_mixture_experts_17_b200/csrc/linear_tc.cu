@@ -60,23 +60,33 @@ __device__ __forceinline__ void tma_4d(void *dst, const void *tmap, int c0, int 
                  : "memory");
 }
 
-__device__ __forceinline__ void tma_3d_pair(void *dst, const void *tmap, int c0, int c1, int c2,
+__device__ __forceinline__ void tma_3d_pair(uint32_t dst, const void *tmap, int c0, int c1, int c2,
                                             uint32_t bar_cluster)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
         : "memory");
 }
 
-__device__ __forceinline__ void tma_4d_pair(void *dst, const void *tmap, int c0, int c1, int c2,
+__device__ __forceinline__ void tma_4d_pair(uint32_t dst, const void *tmap, int c0, int c1, int c2,
                                             int c3, uint32_t bar_cluster)
 {
     asm volatile(
         "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar_cluster)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const void *tmap, int c0, int c1,
+                                            uint32_t bar_cluster)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(bar_cluster)
         : "memory");
 }
 
@@ -105,6 +115,13 @@ template <bool MN>
 __device__ __forceinline__ uint64_t op_desc(uint32_t base, int kk)
 {
     return MN ? smem_desc_mn128(base + kk * 2048) : smem_desc_k128(base + kk * 32);
+}
+
+// What a K step of 16 adds to it (its address field counts 16 bytes).
+template <bool MN>
+__device__ __forceinline__ constexpr uint64_t op_step()
+{
+    return MN ? 2048 / 16 : 32 / 16;
 }
 
 template <LinMode MODE>
@@ -311,10 +328,60 @@ __device__ __forceinline__ void load_bias(const LinOut &o, long long first, int 
 //   warp 2   dW: zeroes the rows of a group's last block past its end
 //   warps 4-11  epilogue, two per TMEM lane quarter, alternating 32 columns
 constexpr int kPairThreads = 384;
-constexpr int kPairStages = 6;
 constexpr int kPairABytes = 2 * kBoxBytes;
-constexpr int kPairStage = 4 * kBoxBytes;   // A and B halves of one CTA
-constexpr int kPairSmem = 1024 + kPairStages * kPairStage + 256 + 8 * kStageBytes;
+constexpr int kRingBytes = 24 * kBoxBytes;
+constexpr int kPairBars = 512;
+constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + 8 * kStageBytes;
+
+// Stages of the ring for tiles of each class (class 0: up to 256 rows; 1: 128; 2:
+// 64): the smaller the tokens' part of a stage, the more stages fit. A stage's round
+// trip (copy, MMAs, commit, the producer's wait) takes 1.9 us even on an idle GPU,
+// so 6 stages of 16 KB of weights let an SM read 51 GB/s, and 9 half as much again.
+// Each class has its own barriers; a CTA goes from one to another at most twice, and
+// only when every stage of the last one has been consumed.
+__host__ __device__ constexpr int ring_stages(int c) { return c == 0 ? 6 : c == 1 ? 8 : 9; }
+__host__ __device__ constexpr int ring_stage_bytes(int c)
+{
+    return kPairABytes + (c == 0 ? 2 * kBoxBytes : c == 1 ? kBoxBytes : kBoxBytes / 2);
+}
+__host__ __device__ constexpr int ring_bar(int c) { return c == 0 ? 0 : c == 1 ? 6 : 14; }
+constexpr int kRingBars = 23;
+
+// A role's place in the ring: its stage's barrier (its index in full and empty), byte
+// offset and the parity of the stage's current use. Kept by steps, not by division:
+// the producer and the MMA issue are one thread each, and what they spend on a stage
+// is not hidden (divisions by a stage count of 6, 8 or 9 cost 8% of 16384 x 14336 -> 4096).
+struct Ring {
+    int cls, bar, at;
+    uint32_t phase;
+    bool used;
+    __device__ __forceinline__ explicit Ring(int c)
+        : cls(c), bar(ring_bar(c)), at(0), phase(0), used(false)
+    {
+    }
+    __device__ __forceinline__ void next()
+    {
+        used = true;
+        ++bar;
+        at += ring_stage_bytes(cls);
+        if (bar == ring_bar(cls) + ring_stages(cls)) {
+            bar = ring_bar(cls);
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+    // the stage before this one
+    __device__ __forceinline__ int last() const
+    {
+        return bar == ring_bar(cls) ? bar + ring_stages(cls) - 1 : bar - 1;
+    }
+    __device__ __forceinline__ uint32_t last_phase() const
+    {
+        return bar == ring_bar(cls) ? phase ^ 1u : phase;
+    }
+};
+static_assert(6 * ring_stage_bytes(0) <= kRingBytes && 8 * ring_stage_bytes(1) <= kRingBytes &&
+                  9 * ring_stage_bytes(2) <= kRingBytes, "the ring holds every class");
 
 struct PairArgs {
     const int32_t *offsets;
@@ -354,17 +421,6 @@ __device__ __forceinline__ int tile_rows(int n)
     return ((n + nt - 1) / nt + 31) & ~31;
 }
 
-// Tile of a pair in a round of npairs tiles. The turn by the golden ratio keeps a
-// pair from meeting one kind of tile only where tile_at mixes two.
-__device__ __forceinline__ int tile_of(int round, int pair, int npairs)
-{
-    const unsigned turn = __umulhi((unsigned)round * 2654435769u, (unsigned)npairs);
-    int at = pair + (int)turn;
-    if (at >= npairs)
-        at -= npairs;
-    return round * npairs + at;
-}
-
 template <LinMode MODE>
 __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G, int t)
 {
@@ -386,15 +442,6 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
         if (a.tail == kBox)
             a.tail = 0;
     } else {
-        // Groups of two or more items are bound by the tensor cores, those of one by
-        // reading their weights: the two are spread evenly over the tiles, so that
-        // they overlap.
-        const int big = G.first[G.nbig] * p.m_tiles, all = G.first[p.E] * p.m_tiles;
-        if (big > 0 && big < all) {
-            const int k = (int)((unsigned long long)t * big / all);
-            const int next = (int)((unsigned long long)(t + 1) * big / all);
-            t = next > k ? k : big + (t - k);
-        }
         const int at = item_group(G, p.E, t / p.m_tiles);
         a.e = G.group[at];
         const int f = G.first[at], ni = G.first[at + 1] - f;
@@ -416,6 +463,43 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
     return a;
 }
 
+// Calls f(tile, class) for a pair's tiles in order, until it returns false. Groups of
+// class 0 are bound by the tensor cores, the others by reading their weights. Where
+// a call has both, the even pairs begin with the one kind and the odd pairs with
+// the other, so that the two overlap and each pair changes its ring only twice.
+template <LinMode MODE, class F>
+__device__ __forceinline__ void walk_tiles(const PairArgs &p, const GroupSmem &G, F f)
+{
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    if (MODE == LIN_DW) {
+        const int total = p.E * p.splits * p.m_tiles * p.c_tiles;
+        for (int t = pair; t < total; t += npairs)
+            if (!f(tile_at<MODE>(p, G, t), 0))
+                return;
+        return;
+    }
+    const bool mixed = npairs > 1 && G.cls[1] > 0 && G.cls[1] < G.cls[3];
+    const bool odd = mixed && (pair & 1);
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) {
+        const int c = odd ? 2 - i : i;
+        int lo = G.cls[c] * p.m_tiles, hi = G.cls[c + 1] * p.m_tiles;
+        int at = pair, step = npairs;
+        if (mixed) {
+            const int even = (npairs + 1) / 2;
+            const int cut = lo + (int)((long long)(hi - lo) * even / npairs);
+            (odd ? lo : hi) = cut;
+            step = odd ? npairs / 2 : even;
+            at = pair >> 1;
+        }
+        if (c)   // the pairs that got one tile more of class 0 get one less here
+            at = step - 1 - at;
+        for (int t = lo + at; t < hi; t += step)
+            if (!f(tile_at<MODE>(p, G, t), c))
+                return;
+    }
+}
+
 template <LinMode MODE, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
@@ -426,24 +510,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __shared__ GroupSmem G;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kPairStages * kPairStage);
-    uint64_t *empty = full + kPairStages;
-    uint64_t *tfull = empty + kPairStages;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRingBytes);
+    uint64_t *empty = full + kRingBars;
+    uint64_t *tfull = empty + kRingBars;
     uint64_t *tempty = tfull + 2;
     uint64_t *tailbar = tempty + 2;   // one a stage: several last blocks may be in flight
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tailbar + kPairStages);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tailbar + ring_stages(0));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    uint8_t *stage = smem + kPairStages * kPairStage + 256;
+    uint8_t *stage = smem + kRingBytes + kPairBars;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < kRingBars; ++s) {
             mbar_init(&full[s], 2);    // the leader's producer twice, or each CTA's warp 2 once
             mbar_init(&empty[s], 1);
-            mbar_init(&tailbar[s], 1);
         }
+        for (int s = 0; s < ring_stages(0); ++s)
+            mbar_init(&tailbar[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);   // 8 epilogue warps of each CTA
@@ -467,50 +552,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_sync_all();   // both CTAs' barriers exist and TMEM is allocated
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = MODE == LIN_DW ? p.E * p.splits * p.m_tiles * p.c_tiles
-                                     : G.first[p.E] * p.m_tiles;
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int rounds = (total + npairs - 1) / npairs;
 
     if (warp == 0) {
         if (lane == 0) {   // ---------------- producer (both CTAs)
-            uint32_t it = 0;
-            for (int i = 0; i < rounds; ++i) {
-                const int t = tile_of(i, pair, npairs);
-                if (t >= total)
-                    break;
-                const TileAt a = tile_at<MODE>(p, G, t);
+            Ring ring(0);
+            const uint32_t smem0 = smem_u32(smem), full0 = mapa_shared(smem_u32(full), 0);
+            walk_tiles<MODE>(p, G, [&](const TileAt &a, int c) {
                 const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
                 const int c0 = a.c0 + (int)rank * half, m0 = a.m0 + 128 * (int)rank;
                 const int fit = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+                const CUtensorMap *tb = &tmB.box[MODE == LIN_DW ? 0 : fit];
                 const int nb = p.b_wide ? 1 : (half + kBox - 1) / kBox;   // LIN_DW: copies of B
                 const uint32_t bytes =
                     kPairABytes + (MODE == LIN_DW ? (p.b_wide ? 2 : nb) * kBoxBytes : 2048 << fit);
-                bool ok = true;
-                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    const uint32_t ph = (it / kPairStages) & 1u;
-                    if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *sa = smem + s * kPairStage, *sb = sa + kPairABytes;
+                if (MODE != LIN_DW && c != ring.cls) {   // another ring over the same memory
+                    if (ring.used && !mbar_wait(&empty[ring.last()], ring.last_phase(), abort_flag, p.status))
+                        return false;
+                    ring = Ring(c);
+                }
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!mbar_wait(&empty[ring.bar], ring.phase ^ 1u, abort_flag, p.status))
+                        return false;
+                    const uint32_t sa = smem0 + ring.at, sb = sa + kPairABytes;
                     const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
-                    uint32_t bar;
+                    uint32_t bar = full0 + ring.bar * 8;
                     if (tail) {   // to this CTA's own barrier; warp 2 passes it on
-                        mbar_arrive_expect_tx(&tailbar[s], bytes);
-                        bar = mapa_shared(smem_u32(&tailbar[s]), rank);
-                    } else {
-                        bar = mapa_shared(smem_u32(&full[s]), 0);
-                        if (leader) {   // for both CTAs' copies: halves are equal
-                            mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                            mbar_arrive(&full[s]);
-                        }
+                        mbar_arrive_expect_tx(&tailbar[ring.bar], bytes);
+                        bar = mapa_shared(smem_u32(&tailbar[ring.bar]), rank);
+                    } else if (leader) {   // for both CTAs' copies: halves are equal
+                        mbar_arrive_expect_tx(&full[ring.bar], 2 * bytes);
+                        mbar_arrive(&full[ring.bar]);
                     }
+                    ring.next();
                     const int k = kb * kBox;
                     if (MODE == LIN_FWD) {
                         tma_3d_pair(sa, &tmA, k, m0, a.e, bar);
-                        tma_load_2d_pair(sb, &tmB.box[fit], k, c0, bar);
+                        tma_2d_pair(sb, tb, k, c0, bar);
                         continue;
                     }
                     const int ka = MODE == LIN_DX ? k : a.r0 + k, ea = MODE == LIN_DX ? a.e : 0;
@@ -521,75 +598,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         tma_4d_pair(sa + kBoxBytes, &tmA, m0 + kBox, ka, 0, ea, bar);
                     }
                     if (MODE == LIN_DX) {
-                        tma_load_2d_pair(sb, &tmB.box[fit], k, c0, bar);
+                        tma_2d_pair(sb, tb, k, c0, bar);
                     } else if (p.b_wide) {
-                        tma_4d_pair(sb, &tmB.box[0], 0, ka, c0 / kBox, 0, bar);
+                        tma_4d_pair(sb, tb, 0, ka, c0 / kBox, 0, bar);
                     } else {
                         for (int j = 0; j < nb; ++j)
-                            tma_4d_pair(sb + j * kBoxBytes, &tmB.box[0], c0 + j * kBox, ka, 0, 0, bar);
+                            tma_4d_pair(sb + j * kBoxBytes, tb, c0 + j * kBox, ka, 0, 0, bar);
                     }
                 }
-                if (!ok)
-                    break;
-            }
+                return true;
+            });
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {   // ---------------- MMA issue
-            uint32_t it = 0, local = 0;
-            for (int i = 0; i < rounds; ++i) {
-                const int t = tile_of(i, pair, npairs);
-                if (t >= total)
-                    break;
-                const TileAt a = tile_at<MODE>(p, G, t);
+            uint32_t local = 0;
+            Ring ring(0);
+            const uint32_t smem0 = smem_u32(smem);
+            walk_tiles<MODE>(p, G, [&](const TileAt &a, int c) {
                 if (MODE == LIN_DW && a.nkb == 0)
-                    continue;            // nothing to add up: the epilogue writes zeros
+                    return true;         // nothing to add up: the epilogue writes zeros
+                if (MODE != LIN_DW && c != ring.cls)
+                    ring = Ring(c);
                 const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
                 ++local;
                 const uint32_t idesc = lin_idesc<MODE>(256, (a.cn + 31) & ~31);
                 if (!mbar_wait_cluster(&tempty[b], aph ^ 1u, abort_flag, p.status))
-                    break;
+                    return false;
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * kTileC;
-                bool ok = true;
-                for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    const uint32_t ph = (it / kPairStages) & 1u;
+                for (int kb = 0; kb < a.nkb; ++kb) {
                     // Copies need no acquire beyond this CTA. One at cluster scope
                     // stalls the issue for longer than a stage's MMAs take, so only
                     // a last block, whose zeros the peer wrote, waits with it.
                     const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
-                    if (!(tail ? mbar_wait_cluster(&full[s], ph, abort_flag, p.status)
-                               : mbar_wait(&full[s], ph, abort_flag, p.status))) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(tail ? mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status)
+                               : mbar_wait(&full[ring.bar], ring.phase, abort_flag, p.status)))
+                        return false;
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + s * kPairStage), b0 = a0 + kPairABytes;
+                    const uint64_t da = op_desc<A_MN>(smem0 + ring.at, 0);
+                    const uint64_t db = op_desc<B_MN>(smem0 + ring.at + kPairABytes, 0);
 #pragma unroll
                     for (int kk = 0; kk < kBox / 16; ++kk)
                         if (!tail || kk * 16 < a.tail)
-                            tc_mma_bf16_pair(d, op_desc<A_MN>(a0, kk), op_desc<B_MN>(b0, kk), idesc,
-                                             (kb | kk) != 0);
-                    tc_commit_pair(&empty[s], 0x3);
+                            tc_mma_bf16_pair(d, da + kk * op_step<A_MN>(), db + kk * op_step<B_MN>(),
+                                             idesc, (kb | kk) != 0);
+                    tc_commit_pair(&empty[ring.bar], 0x3);
+                    ring.next();
                 }
-                if (!ok)
-                    break;
                 tc_commit_pair(&tfull[b], 0x3);
-            }
+                return true;
+            });
         }
     } else if (MODE == LIN_DW && warp == 2) {   // ---------------- last blocks (both CTAs)
         uint32_t it = 0, phases = 0;   // bit s: parity of stage s's next use
-        for (int i = 0; i < rounds; ++i) {
-            const int t = tile_of(i, pair, npairs);
-            if (t >= total)
-                break;
-            const TileAt a = tile_at<MODE>(p, G, t);
+        walk_tiles<MODE>(p, G, [&](const TileAt &a, int) {
             it += a.nkb;
             if (!a.tail)
-                continue;
-            const int s = (it - 1) % kPairStages;
+                return true;
+            const uint32_t s = (it - 1) % ring_stages(0);
             if (!__all_sync(kFullMask, mbar_wait(&tailbar[s], (phases >> s) & 1u, abort_flag, p.status)))
-                break;
+                return false;
             phases ^= 1u << s;
             // row r of a 64 x 64 box is its bytes [128 r, 128 r + 128): the swizzle
             // only permutes the 16-byte pieces of a row. Rows past the last K step of
@@ -598,23 +666,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int boxes = p.b_wide ? 4 : 2 + (((a.cn + 31) & ~31) / 2 + kBox - 1) / kBox;
             for (int r = a.tail + (lane >> 3); r < end; r += 4)
                 for (int j = 0; j < boxes; ++j)
-                    *reinterpret_cast<uint4 *>(smem + s * kPairStage + j * kBoxBytes + r * 128 +
-                                               (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(smem + s * ring_stage_bytes(0) + j * kBoxBytes +
+                                               r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
-        }
+            return true;
+        });
     } else if (warp >= 4) {   // ---------------- epilogue (both CTAs)
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
         const WarpStage ws(stage + (warp - 4) * kStageBytes, lane);
         uint32_t local = 0;
-        for (int i = 0; i < rounds; ++i) {
-            const int t = tile_of(i, pair, npairs);
-            if (t >= total)
-                break;
-            const TileAt a = tile_at<MODE>(p, G, t);
+        walk_tiles<MODE>(p, G, [&](const TileAt &a, int) {
             const int m0 = a.m0 + 128 * (int)rank + q * 32;
             // first row of the output: dW's rows count from expert (and split) 0
             const long long c00 =
@@ -625,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             load_bias<MODE>(p.o, (long long)a.e * p.d_out, m0, M, lane, bias);
             if (!none) {
                 if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
-                    break;
+                    return false;
                 ++local;
                 tc_fence_after();
             }
@@ -647,7 +712,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (lane == 0)
                     mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));
             }
-        }
+            return true;
+        });
     }
 
     __syncthreads();
