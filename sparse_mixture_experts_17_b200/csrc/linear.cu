@@ -23,15 +23,17 @@ namespace {
 // ---------------------------------------------------------------- elementwise backward
 // dz = dy act'(z) in bf16 and the column sums of the unrounded dz over items of
 // kDzRows rows of one group. Bound by HBM: dy and z read, dz written once. A
-// CTA of 8 warps covers 256 columns (a lane 8 of them, 16-byte vectors) and
-// its warps take the item's rows in turn; their sums meet in shared memory in
-// warp order, so db repeats bit for bit.
-constexpr int kDzRows = 64;
+// work unit is 256 columns (a lane 8 of them, 16-byte vectors) of an item; the 8
+// warps take its rows in turn, kDzUnroll in flight each, and their sums meet in
+// shared memory in warp order, so db repeats bit for bit. Persistent: the groups'
+// list is built once a CTA, not once a unit.
+constexpr int kDzRows = 32;
 constexpr int kDzCols = 256;
 constexpr int kDzUnroll = 4;   // rows of a warp in flight
+constexpr int kDzCtasPerSm = 4;
 
 template <int ACT>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, kDzCtasPerSm)
     k_linear_dz(const uint4 *__restrict__ dy, const uint4 *__restrict__ z, uint4 *dz, float *part,
                 const int32_t *offsets, int E, int rows, int d_out, uint32_t *status)
 {
@@ -40,81 +42,95 @@ __global__ void __launch_bounds__(256, 4)
     pdl_wait();
     pdl_trigger();
     build_groups(G, offsets, E, rows, kDzRows, status);
-    const int item = blockIdx.y;
-    if (item >= G.first[E])
-        return;
-    const int e = item_group(G, E, item);
-    const int r0 = G.row0[e] + (item - G.first[e]) * kDzRows;
-    const int r1 = min(r0 + kDzRows, G.row0[e + 1]);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = blockIdx.x * kDzCols + lane * 8, nv = d_out / 8;
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (col < d_out) {
-        const long long at0 = (long long)r0 * nv + col / 8;
-        for (int r = warp; r < r1 - r0; r += 8 * kDzUnroll) {
-            uint4 g[kDzUnroll], zz[kDzUnroll];
+    const int nv = d_out / 8, tiles = (d_out + kDzCols - 1) / kDzCols;
+    const long long units = (long long)G.first[E] * tiles;
+    for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int item = (int)(unit / tiles), tile = (int)(unit - (long long)item * tiles);
+        const int e = item_group(G, E, item);
+        const int r0 = G.row0[e] + (item - G.first[e]) * kDzRows;
+        const int n = min(kDzRows, G.row0[e + 1] - r0);
+        const int col = tile * kDzCols + lane * 8;
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (col < d_out) {
+            const long long at0 = (long long)r0 * nv + col / 8;
+            for (int r = warp; r < n; r += 8 * kDzUnroll) {
+                uint4 g[kDzUnroll], zz[kDzUnroll];
 #pragma unroll
-            for (int u = 0; u < kDzUnroll; ++u)
-                if (r + 8 * u < r1 - r0) {
-                    g[u] = ld_stream_v4(dy + at0 + (long long)(r + 8 * u) * nv);
-                    if (ACT != MOE_ACT_NONE)
-                        zz[u] = ld_stream_v4(z + at0 + (long long)(r + 8 * u) * nv);
-                }
-#pragma unroll
-            for (int u = 0; u < kDzUnroll; ++u)
-                if (r + 8 * u < r1 - r0) {
-                    const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
-                    const uint32_t zw[4] = {zz[u].x, zz[u].y, zz[u].z, zz[u].w};
-                    uint32_t ow[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float a = bf16lo(gw[q]), b = bf16hi(gw[q]);
-                        if (ACT != MOE_ACT_NONE) {
-                            a *= act_grad_f<ACT>(bf16lo(zw[q]));
-                            b *= act_grad_f<ACT>(bf16hi(zw[q]));
-                        }
-                        sum[2 * q] += a;
-                        sum[2 * q + 1] += b;
-                        ow[q] = pack_bf16x2(a, b);
+                for (int u = 0; u < kDzUnroll; ++u)
+                    if (r + 8 * u < n) {
+                        g[u] = ld_stream_v4(dy + at0 + (long long)(r + 8 * u) * nv);
+                        if (ACT != MOE_ACT_NONE)
+                            zz[u] = ld_stream_v4(z + at0 + (long long)(r + 8 * u) * nv);
                     }
-                    if (ACT != MOE_ACT_NONE)
-                        dz[at0 + (long long)(r + 8 * u) * nv] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                }
+#pragma unroll
+                for (int u = 0; u < kDzUnroll; ++u)
+                    if (r + 8 * u < n) {
+                        const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                        const uint32_t zw[4] = {zz[u].x, zz[u].y, zz[u].z, zz[u].w};
+                        uint32_t ow[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float a = bf16lo(gw[q]), b = bf16hi(gw[q]);
+                            if (ACT != MOE_ACT_NONE) {
+                                a *= act_grad_f<ACT>(bf16lo(zw[q]));
+                                b *= act_grad_f<ACT>(bf16hi(zw[q]));
+                            }
+                            sum[2 * q] += a;
+                            sum[2 * q + 1] += b;
+                            ow[q] = pack_bf16x2(a, b);
+                        }
+                        if (ACT != MOE_ACT_NONE)
+                            dz[at0 + (long long)(r + 8 * u) * nv] =
+                                make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                    }
+            }
         }
-    }
-    if (!part)
-        return;
+        if (!part)
+            continue;
+        // a lane's 8 sums lie 32 columns apart, so that neither side has bank conflicts
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        red[warp][lane * 8 + i] = sum[i];
-    __syncthreads();
-    const int c = blockIdx.x * kDzCols + threadIdx.x;
-    if (c < d_out) {
-        float s = 0.f;
+        for (int i = 0; i < 8; ++i)
+            red[warp][i * 32 + lane] = sum[i];
+        __syncthreads();
+        const int c = tile * kDzCols + (threadIdx.x & 31) * 8 + warp;
+        if (c < d_out) {
+            float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
-            s += red[w][threadIdx.x];
-        part[(long long)item * d_out + c] = s;
+            for (int w = 0; w < 8; ++w)
+                s += red[w][threadIdx.x];
+            part[(long long)item * d_out + c] = s;
+        }
+        __syncthreads();
     }
 }
 
-// db[e] = sum of the group's items in order (0 for an empty group).
+// db[e] = sum of the group's items (0 for an empty group). A CTA of 32 columns x 8:
+// each of the 8 adds every eighth item, and their sums are added in order.
 __global__ void __launch_bounds__(256)
     k_linear_db(const float *__restrict__ part, float *db, const int32_t *offsets, int E, int rows,
                 int d_out)
 {
     __shared__ GroupSmem G;
+    __shared__ float red[8][32];
     pdl_wait();
     pdl_trigger();
     build_groups(G, offsets, E, rows, kDzRows, nullptr);
-    const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= d_out)
-        return;
+    const int e = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
-#pragma unroll 8
-    for (int i = G.first[e]; i < G.first[e + 1]; ++i)
-        s += part[(long long)i * d_out + c];
-    db[(long long)e * d_out + c] = s;
+    if (c < d_out)
+#pragma unroll 4
+        for (int i = G.first[e] + w; i < G.first[e + 1]; i += 8)
+            s += part[(long long)i * d_out + c];
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < d_out) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+            s += red[k][lane];
+        db[(long long)e * d_out + c] = s;
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -163,7 +179,9 @@ template <int ACT>
 int launch_dz(const moe_linear_t &s, const uint16_t *dy, const uint16_t *z, uint16_t *dz,
               float *part, const int32_t *offsets, uint32_t *status, cudaStream_t st)
 {
-    launch_pdl_ex(k_linear_dz<ACT>, dim3((s.d_out + kDzCols - 1) / kDzCols, (unsigned)dz_items(s)),
+    const long long units = dz_items(s) * ((s.d_out + kDzCols - 1) / kDzCols);
+    launch_pdl_ex(k_linear_dz<ACT>,
+                  dim3((unsigned)std::min<long long>(units, (long long)kDzCtasPerSm * num_sms())),
                   dim3(256), 0, st, reinterpret_cast<const uint4 *>(dy),
                   reinterpret_cast<const uint4 *>(z), reinterpret_cast<uint4 *>(dz), part, offsets,
                   s.E, s.rows, s.d_out, status);
@@ -274,7 +292,7 @@ int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
             return rc;
     }
     if (dbias) {
-        launch_pdl_ex(k_linear_db, dim3((s.d_out + 255) / 256, s.E), dim3(256), 0, st, part, dbias,
+        launch_pdl_ex(k_linear_db, dim3((s.d_out + 31) / 32, s.E), dim3(256), 0, st, part, dbias,
                       expert_offsets, s.E, s.rows, s.d_out);
         if ((rc = launched()))
             return rc;

@@ -777,18 +777,7 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % p.S;   // clusters run along x
     const int m0 = (blockIdx.x / p.S) * 128;
-    pdl_wait();
-    pdl_trigger();
-    build_groups(G, p.offsets, p.E, p.rows, BC, p.status);
-    const int item = blockIdx.y;
-    if (item >= G.first[p.E])
-        return;                          // the whole cluster: it has one blockIdx.y
-    const int e = item_group(G, p.E, item);
-    const int c0 = G.row0[e] + (item - G.first[e]) * BC;
-    const int cn = min(BC, G.row0[e + 1] - c0);
-    const int per = (p.kblocks + p.S - 1) / p.S;
-    const int k0 = min(rank * per, p.kblocks), nkb = min(k0 + per, p.kblocks) - k0;
-
+    // what needs nothing of the kernel before this one, while that one ends
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -797,15 +786,38 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, BC);
         tmem_relinquish();
     }
+    pdl_wait();
+    pdl_trigger();
+    const int item = blockIdx.y;
+    int e = 0, c0 = item * BC, cn = min(BC, p.rows - c0);
+    bool any = true;
+    if (p.offsets) {
+        build_groups(G, p.offsets, p.E, p.rows, BC, p.status);
+        any = item < G.first[p.E];   // the same for the whole cluster: it has one blockIdx.y
+        if (any) {
+            e = item_group(G, p.E, item);
+            c0 = G.row0[e] + (item - G.first[e]) * BC;
+            cn = min(BC, G.row0[e + 1] - c0);
+        }
+    }
+    const int per = (p.kblocks + p.S - 1) / p.S;
+    const int k0 = min(rank * per, p.kblocks), nkb = min(k0 + per, p.kblocks) - k0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if (!any) {
+        if (warp == 1)
+            tmem_dealloc(tmem_base, BC);
+        return;
+    }
 
     if (warp == 0 && lane == 0) {   // ---------------- producer
         const int nb = (cn + C::BOXROWS - 1) / C::BOXROWS;
@@ -1150,8 +1162,13 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
     const int sms = num_sms();
     if (pair_tiles >= sms / 2 && avg > 32)
         return launch_pair<MODE, ACT>(a, st);
-    const int bc = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
-    const long long tiles = (long long)groups * ceil_div(avg, bc) * ceil_div(M, 128);
+    // tiles no wider than the groups; narrower where that leaves half the SMs without
+    // one (the weights are then read more than once, but from L2)
+    int bc = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
+    const auto tiles_of = [&](int b) { return (long long)groups * ceil_div(avg, b) * ceil_div(M, 128); };
+    while (bc > 32 && tiles_of(bc) * 2 <= sms)
+        bc /= 2;
+    const long long tiles = tiles_of(bc);
     // CTAs that split K: enough to fill the SMs, each with four K stages or more
     int S = 1;
     while (S < 8 && tiles * S * 2 <= (bc == 256 ? sms : 2 * sms) && ceil_div(K, kBox) >= 2 * S * 4)

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from array import array
 import os
 import re
 
@@ -407,13 +408,13 @@ _HERE = contextlib.nullcontext()
 def _args(*specs):
     """Checked pointers of tensors given as (tensor, dtype or None, shape or None, name), and the
     context of _on_one_device. An expected leading axis of 1 may be missing."""
-    ptrs, here = [], -1
-    for t, dtype, shape, name in specs:   # what nearly every call passes, with few steps
+    ptrs, here, Tensor = [], -1, torch.Tensor
+    for t, dtype, shape, _ in specs:   # what nearly every call passes, with few steps
         if t is None:
             ptrs.append(None)
             continue
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and
-                (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
+        if not (isinstance(t, Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and
+                (shape is None or t.shape == shape) and t.is_contiguous()):
             break
         if here < 0:
             here = torch.cuda.current_device()
@@ -518,16 +519,18 @@ _KINDS = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
 def _tensor_list(tensors, name):
     """(pointers, element counts, MOE_TYPE_*) of fp32 / bf16 tensors on one device, as host
     arrays."""
-    ptrs, _ = _args(*((t, None, None, name) for t in tensors))
-    n = len(tensors)
+    ptrs, _ = _args(*[(t, None, None, name) for t in tensors])
     types = []
     for i, t in enumerate(tensors):
         if t is None or t.dtype not in _KINDS:
             raise TypeError(f"{name}[{i}]: expected float32 or bfloat16, got "
                             f"{None if t is None else t.dtype}")
         types.append(_KINDS[t.dtype])
-    return ((_P * n)(*ptrs), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * n)(*types))
+    return array("Q", ptrs), array("q", [t.numel() for t in tensors]), array("i", types)
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def alloc_grad_workspace(grads=(), device="cuda") -> torch.Tensor:
@@ -547,7 +550,8 @@ def moe_grad_norm(grads, norm, status=None, ws=None, stream=None):
         *((t, None, None, "grads") for t in grads[:1]))
     with on_device:
         _check("moe_grad_norm", lib().moe_grad_norm(
-            len(grads), ptrs, numel, types, norm_p, status_p, ws_p, _nbytes(ws), _stream(stream)))
+            len(grads), _address(ptrs), _address(numel), _address(types), norm_p, status_p, ws_p,
+            _nbytes(ws), _stream(stream)))
     return norm
 
 
@@ -564,7 +568,7 @@ def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, strea
         for i, (g, o) in enumerate(zip(grads, outs)):
             if g.dtype != o.dtype or g.numel() != o.numel():
                 raise ValueError(f"outs[{i}]: must match grads[{i}] in type and size")
-        optrs = _tensor_list(outs, "outs")[0]
+        optrs, _, _ = _tensor_list(outs, "outs")
         firsts = firsts + outs[:1]
     _at_least(norm, 1, "norm")
     _at_least(status, 1, "status")
@@ -573,8 +577,8 @@ def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, strea
         *((t, None, None, "grads / outs") for t in firsts))
     with on_device:
         _check("moe_clip_grads", lib().moe_clip_grads(
-            len(grads), ptrs, optrs, numel, types, float(max_norm), norm_p, status_p, ws_p,
-            _nbytes(ws), _stream(stream)))
+            len(grads), _address(ptrs), _address(optrs), _address(numel), _address(types),
+            float(max_norm), norm_p, status_p, ws_p, _nbytes(ws), _stream(stream)))
     return norm
 
 
