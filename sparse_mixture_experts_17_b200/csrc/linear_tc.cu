@@ -96,6 +96,14 @@ __device__ __forceinline__ void fence_proxy_async()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Arrive on a barrier of another CTA of the cluster without ordering memory at cluster
+// scope: a release there would wait until the warp's stores to global memory are done.
+// For hand-overs of tensor memory, which carry no data through memory.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // MN-major operand in 128-byte-swizzled boxes of 64 (MN) x 64 (K): 8 K rows of
 // 128 bytes per 1024-byte atom (stride offset 1024 between atoms along K), the
 // next 64 MN elements one box further (leading offset 8192).
@@ -209,13 +217,20 @@ __device__ __forceinline__ void copy_out(const WarpStage &w, uint16_t *dst, long
     __syncwarp();
 }
 
-// Columns [0, n) of the accumulator at taddr, n <= 32, to rows c0 + [0, n) of m
-// [m0, m0 + 32) cut at M. bias[i]: of m0 + 8 i + lane / 4. With `zero` the
-// accumulator holds nothing and the result is 0.
-template <LinMode MODE, int ACT>
-__device__ __forceinline__ void store_chunk(const LinOut &o, uint32_t taddr, bool zero,
+// 32 lanes x 32 columns of an accumulator; tmem_ld_wait() before v is used.
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[2][16])
+{
+    tmem_ld16(taddr, v[0]);
+    tmem_ld16(taddr + (16u << 16), v[1]);
+}
+
+// Columns [0, n) of an accumulator, n <= 32, to rows c0 + [0, n) of m [m0, m0 + 32)
+// cut at M. bias[i]: of m0 + 8 i + lane / 4. `loaded` runs between the residual's
+// loads and the first use of v.
+template <LinMode MODE, int ACT, class F>
+__device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][16],
                                             const float (&bias)[4], long long c0, int m0, int M,
-                                            int n, int lane, const WarpStage &w)
+                                            int n, int lane, const WarpStage &w, F loaded)
 {
     const int m = m0 + (lane & 3) * 8;
     // rows this lane moves: c = lane / 4 + 8 i < n, none when its m lie past the end
@@ -228,16 +243,7 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, uint32_t taddr, boo
             if (8 * i < rows)
                 res[i] = *reinterpret_cast<const uint4 *>(o.residual + at + i * ld8);
     }
-    float v[2][16];
-    if (zero) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            v[0][i] = v[1][i] = 0.f;
-    } else {
-        tmem_ld16(taddr, v[0]);
-        tmem_ld16(taddr + (16u << 16), v[1]);
-        tmem_ld_wait();
-    }
+    loaded();
     if (MODE == LIN_FWD) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -281,6 +287,47 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, uint32_t taddr, boo
         stmatrix4_t(w.mat + ci * 512, r);
     }
     copy_out(w, o.out + at, ld8, rows);
+}
+
+// A warp's part of a tile: columns h * 32 + [0, 32), and every 64 from there, below cn.
+// Two chunks' loads go out together where the registers allow it, and `release` runs
+// as soon as the last value has left the accumulator.
+template <LinMode MODE, int ACT, class R>
+__device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
+                                           const float (&bias)[4], long long c0, int m0, int M,
+                                           int cn, int lane, const WarpStage &w, R release)
+{
+    constexpr int STEP = MODE == LIN_FWD ? 64 : 128;
+    const int first = h * 32;
+    if (m0 >= M || first >= cn) {
+        release();
+        return;
+    }
+#pragma unroll 1
+    for (int c = first; c < cn; c += STEP) {
+        float v[2][16], v2[2][16];
+        load_acc(tb + c, v);
+        const bool two = MODE != LIN_FWD && c + 64 < cn;
+        if (two)
+            load_acc(tb + c + 64, v2);
+        store_chunk<MODE, ACT>(o, v, bias, c0 + c, m0, M, min(32, cn - c), lane, w, [&] {
+            tmem_ld_wait();
+            if (c + STEP >= cn)
+                release();
+        });
+        if (two)
+            store_chunk<MODE, ACT>(o, v2, bias, c0 + c + 64, m0, M, min(32, cn - c - 64), lane, w,
+                                   [] {});
+    }
+}
+
+// Zeros in place of a tile: the gradient of an empty group's weights.
+__device__ __forceinline__ void store_zeros(const LinOut &o, int h, long long c0, int m0, int M, int cn,
+                                            int lane)
+{
+    const int m = m0 + (lane & 3) * 8;
+    for (int c = h * 8 + (lane >> 2); c < cn && m < M; c += 16)
+        *reinterpret_cast<uint4 *>(o.out + (c0 + c) * o.ld + m) = make_uint4(0, 0, 0, 0);
 }
 
 // The same for fp32 partial sums of dW: a lane holds one m of 32 columns, and a
@@ -383,6 +430,17 @@ struct Ring {
 static_assert(6 * ring_stage_bytes(0) <= kRingBytes && 8 * ring_stage_bytes(1) <= kRingBytes &&
                   9 * ring_stage_bytes(2) <= kRingBytes, "the ring holds every class");
 
+// n / d for 0 <= n < 2^31 by a multiplication: n (ceil(2^64 / d) / 2^64 - 1 / d) < 2^-32
+// cannot reach the next integer.
+struct Divisor {
+    unsigned long long inv;   // 0: d = 1
+    void set(int d) { inv = d == 1 ? 0 : ~0ull / (unsigned)d + 1; }
+    __device__ __forceinline__ int div(int n) const
+    {
+        return inv ? (int)__umul64hi((unsigned long long)n, inv) : n;
+    }
+};
+
 struct PairArgs {
     const int32_t *offsets;
     int E, rows, d_in, d_out;
@@ -391,6 +449,7 @@ struct PairArgs {
     int kblocks;     // LIN_FWD, LIN_DX
     int band;        // items of a group whose B rows stay in L2 while W passes by
     int splits;      // LIN_DW
+    Divisor by_m, by_c, by_split;   // m_tiles, c_tiles, splits
     bool a_wide, b_wide;   // MN-major operands: two boxes in one copy
     LinOut o;
     uint32_t *status;
@@ -426,15 +485,14 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
 {
     TileAt a;
     if (MODE == LIN_DW) {
-        const int per = p.m_tiles * p.c_tiles;
-        const int g = t / per, r = t - g * per;
-        a.e = g / p.splits;
+        const int cg = p.by_m.div(t), g = p.by_c.div(cg);
+        a.e = p.by_split.div(g);
         a.split = g - a.e * p.splits;
-        a.m0 = (r % p.m_tiles) * 256;
-        a.c0 = (r / p.m_tiles) * kTileC;
+        a.m0 = (t - cg * p.m_tiles) * 256;
+        a.c0 = (cg - g * p.c_tiles) * kTileC;
         a.cn = min(kTileC, p.d_out - a.c0);
         const int first = G.row0[a.e], n = G.row0[a.e + 1] - first;
-        const int all = (n + kBox - 1) / kBox, part = (all + p.splits - 1) / p.splits;
+        const int all = (n + kBox - 1) / kBox, part = p.by_split.div(all + p.splits - 1);
         const int k0 = min(a.split * part, all), k1 = min(k0 + part, all);
         a.nkb = k1 - k0;
         a.r0 = first + k0 * kBox;
@@ -442,7 +500,7 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
         if (a.tail == kBox)
             a.tail = 0;
     } else {
-        const int at = item_group(G, p.E, t / p.m_tiles);
+        const int at = item_group(G, p.E, p.by_m.div(t));
         a.e = G.group[at];
         const int f = G.first[at], ni = G.first[at + 1] - f;
         const int local = t - f * p.m_tiles;
@@ -622,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
                 ++local;
                 const uint32_t idesc = lin_idesc<MODE>(256, (a.cn + 31) & ~31);
-                if (!mbar_wait_cluster(&tempty[b], aph ^ 1u, abort_flag, p.status))
+                if (!mbar_wait(&tempty[b], aph ^ 1u, abort_flag, p.status))
                     return false;
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * kTileC;
@@ -695,22 +753,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 tc_fence_after();
             }
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kTileC;
-            if (m0 < M) {
-#pragma unroll 1
-                for (int c = h * 32; c < a.cn; c += 64) {
-                    const int n = min(32, a.cn - c);
-                    if (MODE == LIN_DW && p.o.part)
-                        store_part(p.o.part, p.o.ld, tb + c, none, c00 + a.c0 + c, m0 + lane, M, n);
-                    else
-                        store_chunk<MODE, ACT>(p.o, tb + c, none, bias, c00 + a.c0 + c, m0, M, n,
-                                               lane, ws);
-                }
-            }
-            if (!none) {
+            const auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[b]), 0));
+                    mbar_arrive_remote(mapa_shared(smem_u32(&tempty[b]), 0));
+            };
+            if (MODE == LIN_DW && p.o.part) {
+                for (int c = h * 32; c < a.cn && m0 < M; c += 64)
+                    store_part(p.o.part, p.o.ld, tb + c, none, c00 + a.c0 + c, m0 + lane, M,
+                               min(32, a.cn - c));
+                if (!none)
+                    release();
+            } else if (none) {
+                store_zeros(p.o, h, c00 + a.c0, m0, M, a.cn, lane);
+            } else {
+                store_tile<MODE, ACT>(p.o, tb, h, bias, c00 + a.c0, m0, M, a.cn, lane, ws, release);
             }
             return true;
         });
@@ -874,12 +932,8 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         const int mq = m0 + q * 32;
         float bias[4];
         load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
-        if (got && mq < M) {
-#pragma unroll 1
-            for (int c = h * 32; c < cn; c += 64)
-                store_chunk<MODE, ACT>(p.o, tb + c, false, bias, c0 + c, mq, M, min(32, cn - c), lane,
-                                       ws);
-        }
+        if (got)
+            store_tile<MODE, ACT>(p.o, tb, h, bias, c0, mq, M, cn, lane, ws, [] {});
     } else {
         // partial sums [c][128 m] over the ring, which every copy and MMA has left
         float *mine = reinterpret_cast<float *>(smem);
@@ -1086,6 +1140,9 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
     // a band's token rows stay in L2 (48 MiB of them) while it sweeps the m tiles
     p.band = (int)std::max<long long>((48LL << 20) / ((long long)kTileC * K * 2), 1);
     p.splits = std::max(a.splits, 1);
+    p.by_m.set(p.m_tiles);
+    p.by_c.set(p.c_tiles);
+    p.by_split.set(p.splits);
     p.a_wide = a_wide;
     p.b_wide = b_wide;
     p.o = out_of(MODE, a);
