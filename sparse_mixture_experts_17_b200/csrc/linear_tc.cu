@@ -377,7 +377,7 @@ __device__ __forceinline__ void load_bias(const LinOut &o, long long first, int 
 constexpr int kPairThreads = 384;
 constexpr int kPairABytes = 2 * kBoxBytes;
 constexpr int kRingBytes = 24 * kBoxBytes;
-constexpr int kPairBars = 512;
+constexpr int kPairBars = 768;
 constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + 8 * kStageBytes;
 
 // Stages of the ring for tiles of each class (class 0: up to 256 rows; 1: 128; 2:
@@ -386,13 +386,15 @@ constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + 8 * kStageBytes;
 // so 6 stages of 16 KB of weights let an SM read 51 GB/s, and 9 half as much again.
 // Each class has its own barriers; a CTA goes from one to another at most twice, and
 // only when every stage of the last one has been consumed.
-__host__ __device__ constexpr int ring_stages(int c) { return c == 0 ? 6 : c == 1 ? 8 : 9; }
+// Class 3 is for double tiles (up to 512 rows).
+__host__ __device__ constexpr int ring_stages(int c) { return c == 0 ? 6 : c == 1 ? 8 : c == 2 ? 9 : 4; }
 __host__ __device__ constexpr int ring_stage_bytes(int c)
 {
-    return kPairABytes + (c == 0 ? 2 * kBoxBytes : c == 1 ? kBoxBytes : kBoxBytes / 2);
+    return kPairABytes +
+           (c == 0 ? 2 * kBoxBytes : c == 1 ? kBoxBytes : c == 2 ? kBoxBytes / 2 : 4 * kBoxBytes);
 }
-__host__ __device__ constexpr int ring_bar(int c) { return c == 0 ? 0 : c == 1 ? 6 : 14; }
-constexpr int kRingBars = 23;
+__host__ __device__ constexpr int ring_bar(int c) { return c == 0 ? 0 : c == 1 ? 6 : c == 2 ? 14 : 23; }
+constexpr int kRingBars = 27;
 
 // A role's place in the ring: its stage's barrier (its index in full and empty), byte
 // offset and the parity of the stage's current use. Kept by steps, not by division:
@@ -428,7 +430,9 @@ struct Ring {
     }
 };
 static_assert(6 * ring_stage_bytes(0) <= kRingBytes && 8 * ring_stage_bytes(1) <= kRingBytes &&
-                  9 * ring_stage_bytes(2) <= kRingBytes, "the ring holds every class");
+                  9 * ring_stage_bytes(2) <= kRingBytes && 4 * ring_stage_bytes(3) <= kRingBytes,
+              "the ring holds every class");
+static_assert((2 * kRingBars + 4 + ring_stages(0)) * 8 + 8 <= kPairBars, "room for the barriers");
 
 // n / d for 0 <= n < 2^31 by a multiplication: n (ceil(2^64 / d) / 2^64 - 1 / d) < 2^-32
 // cannot reach the next integer.
@@ -470,6 +474,7 @@ struct TileAt {
     int r0;           // LIN_DW: first row of the contraction
     int nkb, tail;    // K blocks; LIN_DW: rows of the last block (0: all 64)
     int split;
+    int cn2;          // double tile: rows of its second half, which follow the first's; else 0
 };
 
 // Rows of one token tile of a group of n rows: near-equal tiles of at most 256,
@@ -480,7 +485,7 @@ __device__ __forceinline__ int tile_rows(int n)
     return ((n + nt - 1) / nt + 31) & ~31;
 }
 
-template <LinMode MODE>
+template <LinMode MODE, bool WIDE>
 __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G, int t)
 {
     TileAt a;
@@ -488,6 +493,7 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
         const int cg = p.by_m.div(t), g = p.by_c.div(cg);
         a.e = p.by_split.div(g);
         a.split = g - a.e * p.splits;
+        a.cn2 = 0;
         a.m0 = (t - cg * p.m_tiles) * 256;
         a.c0 = (cg - g * p.c_tiles) * kTileC;
         a.cn = min(kTileC, p.d_out - a.c0);
@@ -511,8 +517,10 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
         a.m0 = (r / in_band) * 256;
         const int first = G.row0[a.e], n = G.row0[a.e + 1] - first;
         const int q = tile_rows(n);
-        a.c0 = first + i * q;
-        a.cn = min(q, n - i * q);
+        const int c = (WIDE ? 2 * i : i) * q;
+        a.c0 = first + c;
+        a.cn = min(q, n - c);
+        a.cn2 = WIDE ? max(min(q, n - c - q), 0) : 0;
         a.nkb = p.kblocks;
         a.r0 = 0;
         a.tail = 0;
@@ -525,14 +533,14 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
 // class 0 are bound by the tensor cores, the others by reading their weights. Where
 // a call has both, the even pairs begin with the one kind and the odd pairs with
 // the other, so that the two overlap and each pair changes its ring only twice.
-template <LinMode MODE, class F>
+template <LinMode MODE, bool WIDE, class F>
 __device__ __forceinline__ void walk_tiles(const PairArgs &p, const GroupSmem &G, F f)
 {
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (MODE == LIN_DW) {
         const int total = p.E * p.splits * p.m_tiles * p.c_tiles;
         for (int t = pair; t < total; t += npairs)
-            if (!f(tile_at<MODE>(p, G, t), 0))
+            if (!f(tile_at<MODE, WIDE>(p, G, t), 0))
                 return;
         return;
     }
@@ -553,12 +561,12 @@ __device__ __forceinline__ void walk_tiles(const PairArgs &p, const GroupSmem &G
         if (c)   // the pairs that got one tile more of class 0 get one less here
             at = step - 1 - at;
         for (int t = lo + at; t < hi; t += step)
-            if (!f(tile_at<MODE>(p, G, t), c))
+            if (!f(tile_at<MODE, WIDE>(p, G, t), WIDE && c == 0 ? 3 : c))
                 return;
     }
 }
 
-template <LinMode MODE, int ACT>
+template <LinMode MODE, int ACT, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps tmB,
                   const PairArgs p)
@@ -605,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pdl_wait();
     pdl_trigger();
     // items of one group: token tiles; LIN_DW needs the groups' rows only
-    build_groups<true>(G, p.offsets, p.E, p.rows, kTileC, p.status);
+    build_groups<true>(G, p.offsets, p.E, p.rows, WIDE ? 2 * kTileC : kTileC, p.status);
     tc_fence_before();
     cluster_sync_all();   // both CTAs' barriers exist and TMEM is allocated
     tc_fence_after();
@@ -613,16 +621,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {   // ---------------- producer (both CTAs)
-            Ring ring(0);
+            Ring ring(WIDE ? 3 : 0);
             const uint32_t smem0 = smem_u32(smem), full0 = mapa_shared(smem_u32(full), 0);
-            walk_tiles<MODE>(p, G, [&](const TileAt &a, int c) {
+            walk_tiles<MODE, WIDE>(p, G, [&](const TileAt &a, int c) {
                 const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
                 const int c0 = a.c0 + (int)rank * half, m0 = a.m0 + 128 * (int)rank;
                 const int fit = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
                 const CUtensorMap *tb = &tmB.box[MODE == LIN_DW ? 0 : fit];
                 const int nb = p.b_wide ? 1 : (half + kBox - 1) / kBox;   // LIN_DW: copies of B
+                const int half2 = WIDE ? ((a.cn2 + 31) & ~31) / 2 : 0;
+                const int c2 = a.c0 + a.cn + (int)rank * half2;
+                const int fit2 = half2 <= 16 ? 0 : half2 <= 32 ? 1 : half2 <= 64 ? 2 : 3;
                 const uint32_t bytes =
-                    kPairABytes + (MODE == LIN_DW ? (p.b_wide ? 2 : nb) * kBoxBytes : 2048 << fit);
+                    kPairABytes + (MODE == LIN_DW ? (p.b_wide ? 2 : nb) * kBoxBytes : 2048 << fit) +
+                    (half2 ? 2048 << fit2 : 0);
                 if (MODE != LIN_DW && c != ring.cls) {   // another ring over the same memory
                     if (ring.used && !mbar_wait(&empty[ring.last()], ring.last_phase(), abort_flag, p.status))
                         return false;
@@ -643,6 +655,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                     ring.next();
                     const int k = kb * kBox;
+                    if (WIDE && half2)
+                        tma_2d_pair(sb + 2 * kBoxBytes, &tmB.box[fit2], k, c2, bar);
                     if (MODE == LIN_FWD) {
                         tma_3d_pair(sa, &tmA, k, m0, a.e, bar);
                         tma_2d_pair(sb, tb, k, c0, bar);
@@ -670,9 +684,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && leader) {   // ---------------- MMA issue
             uint32_t local = 0;
-            Ring ring(0);
+            Ring ring(WIDE ? 3 : 0);
             const uint32_t smem0 = smem_u32(smem);
-            walk_tiles<MODE>(p, G, [&](const TileAt &a, int c) {
+            // the K steps of one stage into the accumulator at d; B at boff of the stage
+            const auto mma = [&](uint32_t d, uint32_t idesc, const Ring &r, uint32_t boff, bool add,
+                                 int rows) {
+                const uint64_t da = op_desc<A_MN>(smem0 + r.at, 0);
+                const uint64_t db = op_desc<B_MN>(smem0 + r.at + boff, 0);
+#pragma unroll
+                for (int kk = 0; kk < kBox / 16; ++kk)
+                    if (kk * 16 < rows)
+                        tc_mma_bf16_pair(d, da + kk * op_step<A_MN>(), db + kk * op_step<B_MN>(), idesc,
+                                         add || kk != 0);
+            };
+            const auto wait_full = [&](const Ring &r) {
+                const bool ok = mbar_wait(&full[r.bar], r.phase, abort_flag, p.status);
+                tc_fence_after();
+                return ok;
+            };
+            walk_tiles<MODE, WIDE>(p, G, [&](const TileAt &a, int c) {
                 if (MODE == LIN_DW && a.nkb == 0)
                     return true;         // nothing to add up: the epilogue writes zeros
                 if (MODE != LIN_DW && c != ring.cls)
@@ -684,24 +714,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     return false;
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * kTileC;
-                for (int kb = 0; kb < a.nkb; ++kb) {
+                if (WIDE && a.cn2) {
+                    // Both accumulators at work: the first four stages go into the first
+                    // one while the epilogue may still read the second, and the last four
+                    // finish the first one early.
+                    const uint32_t b2 = local & 1u, aph2 = (local >> 1) & 1u;
+                    ++local;
+                    const uint32_t idesc2 = lin_idesc<MODE>(256, (a.cn2 + 31) & ~31);
+                    const uint32_t d2 = tmem_base + b2 * kTileC, boff2 = kPairABytes + 2 * kBoxBytes;
+                    const int head = min(a.nkb, ring_stages(3));
+                    const int tail = a.nkb >= 2 * ring_stages(3) ? ring_stages(3) : 0;
+                    Ring r = ring;
+                    for (int kb = 0; kb < head; ++kb, r.next()) {
+                        if (!wait_full(r))
+                            return false;
+                        mma(d, idesc, r, kPairABytes, kb != 0, kBox);
+                    }
+                    if (!mbar_wait(&tempty[b2], aph2 ^ 1u, abort_flag, p.status))
+                        return false;
+                    tc_fence_after();
+                    for (int kb = 0; kb < head; ++kb, ring.next()) {
+                        mma(d2, idesc2, ring, boff2, kb != 0, kBox);
+                        tc_commit_pair(&empty[ring.bar], 0x3);
+                    }
+                    for (int kb = head; kb < a.nkb - tail; ++kb, ring.next()) {
+                        if (!wait_full(ring))
+                            return false;
+                        mma(d, idesc, ring, kPairABytes, true, kBox);
+                        mma(d2, idesc2, ring, boff2, true, kBox);
+                        tc_commit_pair(&empty[ring.bar], 0x3);
+                    }
+                    r = ring;
+                    for (int kb = 0; kb < tail; ++kb, r.next()) {
+                        if (!wait_full(r))
+                            return false;
+                        mma(d, idesc, r, kPairABytes, true, kBox);
+                    }
+                    tc_commit_pair(&tfull[b], 0x3);
+                    for (int kb = 0; kb < tail; ++kb, ring.next()) {
+                        mma(d2, idesc2, ring, boff2, true, kBox);
+                        tc_commit_pair(&empty[ring.bar], 0x3);
+                    }
+                    tc_commit_pair(&tfull[b2], 0x3);
+                    return true;
+                }
+                for (int kb = 0; kb < a.nkb; ++kb, ring.next()) {
                     // Copies need no acquire beyond this CTA. One at cluster scope
                     // stalls the issue for longer than a stage's MMAs take, so only
                     // a last block, whose zeros the peer wrote, waits with it.
-                    const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
-                    if (!(tail ? mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status)
-                               : mbar_wait(&full[ring.bar], ring.phase, abort_flag, p.status)))
+                    const bool last = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
+                    if (last && !mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status))
                         return false;
-                    tc_fence_after();
-                    const uint64_t da = op_desc<A_MN>(smem0 + ring.at, 0);
-                    const uint64_t db = op_desc<B_MN>(smem0 + ring.at + kPairABytes, 0);
-#pragma unroll
-                    for (int kk = 0; kk < kBox / 16; ++kk)
-                        if (!tail || kk * 16 < a.tail)
-                            tc_mma_bf16_pair(d, da + kk * op_step<A_MN>(), db + kk * op_step<B_MN>(),
-                                             idesc, (kb | kk) != 0);
+                    if (!wait_full(ring))
+                        return false;
+                    mma(d, idesc, ring, kPairABytes, kb != 0, last ? a.tail : kBox);
                     tc_commit_pair(&empty[ring.bar], 0x3);
-                    ring.next();
                 }
                 tc_commit_pair(&tfull[b], 0x3);
                 return true;
@@ -709,7 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else if (MODE == LIN_DW && warp == 2) {   // ---------------- last blocks (both CTAs)
         uint32_t it = 0, phases = 0;   // bit s: parity of stage s's next use
-        walk_tiles<MODE>(p, G, [&](const TileAt &a, int) {
+        walk_tiles<MODE, WIDE>(p, G, [&](const TileAt &a, int) {
             it += a.nkb;
             if (!a.tail)
                 return true;
@@ -737,38 +804,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
         const WarpStage ws(stage + (warp - 4) * kStageBytes, lane);
         uint32_t local = 0;
-        walk_tiles<MODE>(p, G, [&](const TileAt &a, int) {
+        walk_tiles<MODE, WIDE>(p, G, [&](const TileAt &a, int) {
             const int m0 = a.m0 + 128 * (int)rank + q * 32;
             // first row of the output: dW's rows count from expert (and split) 0
             const long long c00 =
                 MODE == LIN_DW ? ((long long)(p.o.part ? a.split * p.E : 0) + a.e) * p.d_out : 0;
             const bool none = MODE == LIN_DW && a.nkb == 0;
-            const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
             float bias[4];
             load_bias<MODE>(p.o, (long long)a.e * p.d_out, m0, M, lane, bias);
-            if (!none) {
-                if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
-                    return false;
-                ++local;
-                tc_fence_after();
-            }
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kTileC;
-            const auto release = [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_remote(mapa_shared(smem_u32(&tempty[b]), 0));
-            };
-            if (MODE == LIN_DW && p.o.part) {
-                for (int c = h * 32; c < a.cn && m0 < M; c += 64)
-                    store_part(p.o.part, p.o.ld, tb + c, none, c00 + a.c0 + c, m0 + lane, M,
-                               min(32, a.cn - c));
-                if (!none)
-                    release();
-            } else if (none) {
-                store_zeros(p.o, h, c00 + a.c0, m0, M, a.cn, lane);
-            } else {
-                store_tile<MODE, ACT>(p.o, tb, h, bias, c00 + a.c0, m0, M, a.cn, lane, ws, release);
+            for (int part = 0; part < (WIDE && a.cn2 ? 2 : 1); ++part) {   // one, or the two of a double tile
+                const int cn = part ? a.cn2 : a.cn;
+                const long long c0 = c00 + a.c0 + (part ? a.cn : 0);
+                const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
+                if (!none) {
+                    if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
+                        return false;
+                    ++local;
+                    tc_fence_after();
+                }
+                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kTileC;
+                const auto release = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_remote(mapa_shared(smem_u32(&tempty[b]), 0));
+                };
+                if (MODE == LIN_DW && p.o.part) {
+                    for (int c = h * 32; c < cn && m0 < M; c += 64)
+                        store_part(p.o.part, p.o.ld, tb + c, none, c0 + c, m0 + lane, M,
+                                   min(32, cn - c));
+                    if (!none)
+                        release();
+                } else if (none) {
+                    store_zeros(p.o, h, c0, m0, M, cn, lane);
+                } else {
+                    store_tile<MODE, ACT>(p.o, tb, h, bias, c0, m0, M, cn, lane, ws, release);
+                }
             }
             return true;
         });
@@ -1107,7 +1178,7 @@ int token_map(LinMode mode, const LinArgs &a, int box_rows, CUtensorMap *B)
                            : make_map(B, a.dz, a.d_out, a.rows, 0, box_rows);
 }
 
-template <LinMode MODE, int ACT>
+template <LinMode MODE, int ACT, bool WIDE = false>
 int launch_pair(const LinArgs &a, cudaStream_t st)
 {
     CUtensorMap A;
@@ -1124,7 +1195,7 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
         rc = make_map_mn(&B.box[0], a.dz, a.d_out, a.rows, 1, b_wide);
     for (int i = 0; i < 4 && !rc && MODE != LIN_DW; ++i)
         rc = token_map(MODE, a, 16 << i, &B.box[i]);
-    if (rc || (rc = allow_smem(k_linear_pair<MODE, ACT>, kPairSmem)))
+    if (rc || (rc = allow_smem(k_linear_pair<MODE, ACT, WIDE>, kPairSmem)))
         return rc;
     PairArgs p;
     std::memset(&p, 0, sizeof p);
@@ -1138,7 +1209,7 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
     const int K = MODE == LIN_FWD ? a.d_in : a.d_out;
     p.kblocks = ceil_div(K, kBox);
     // a band's token rows stay in L2 (48 MiB of them) while it sweeps the m tiles
-    p.band = (int)std::max<long long>((48LL << 20) / ((long long)kTileC * K * 2), 1);
+    p.band = (int)std::max<long long>((48LL << 20) / ((long long)(WIDE ? 2 : 1) * kTileC * K * 2), 1);
     p.splits = std::max(a.splits, 1);
     p.by_m.set(p.m_tiles);
     p.by_c.set(p.c_tiles);
@@ -1151,7 +1222,7 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
         MODE == LIN_DW ? (long long)a.E * p.splits * p.m_tiles * p.c_tiles
                        : (long long)(ceil_div(a.rows, kTileC) + std::min(a.E, a.rows)) * p.m_tiles;
     const int pairs = (int)std::min<long long>(tiles, num_sms() / 2);
-    launch_pdl_ex(k_linear_pair<MODE, ACT>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, A, B, p);
+    launch_pdl_ex(k_linear_pair<MODE, ACT, WIDE>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, A, B, p);
     if ((rc = launched()))
         return rc;
     if (MODE == LIN_DW && p.splits > 1) {
@@ -1217,8 +1288,18 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
     const int avg = ceil_div(a.rows, groups);
     const long long pair_tiles = (long long)groups * ceil_div(avg, kTileC) * ceil_div(M, 256);
     const int sms = num_sms();
-    if (pair_tiles >= sms / 2 && avg > 32)
+    if (pair_tiles >= sms / 2 && avg > 32) {
+        // Double tiles share the weights' part of a stage between 512 rows: a quarter less
+        // from L2 for the same products, at the price of an epilogue that overlaps less.
+        // us single -> double: 16384 x 14336 -> 4096 1842 -> 1618, 4096 x 8192 -> 4096 in 8
+        // groups 307 -> 276, 16384 x 4096 -> 4096 554 -> 520, x 2048 297 -> 298, x 1024 170 ->
+        // 185; where the pairs' last round fills up worse (8192 x 2048 -> 4096 in 8) 154 -> 170.
+        const long long pairs = sms / 2, half = (pair_tiles + 1) / 2;
+        if (avg >= 2 * kTileC && ceil_div(K, kBox) >= 64 &&
+            2 * ((half + pairs - 1) / pairs) <= (pair_tiles + pairs - 1) / pairs)
+            return launch_pair<MODE, ACT, true>(a, st);
         return launch_pair<MODE, ACT>(a, st);
+    }
     // tiles no wider than the groups; narrower where that leaves half the SMs without
     // one (the weights are then read more than once, but from L2)
     int bc = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
