@@ -139,19 +139,17 @@ __device__ __forceinline__ uint32_t lin_idesc(int M, int N)
            | (MODE == LIN_DW ? 1u << 16 : 0u);                        // B is MN-major
 }
 
-// 16 TMEM lanes (m) x 32 columns (c): in v[4 i + j], j = 0, 1: lane t / 4, column
+// 16 TMEM lanes (m) x 16 columns (c): in v[4 i + j], j = 0, 1: lane t / 4, column
 // 8 i + 2 (t % 4) + j; j = 2, 3: the same columns of lane t / 4 + 8 (t: this thread).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[8])
 {
-    uint32_t r[16];
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                   "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
         v[i] = __uint_as_float(r[i]);
 }
 
@@ -182,16 +180,18 @@ struct LinOut {
     long long ld;       // elements between consecutive c
 };
 
-// A warp turns 32 m (its TMEM lanes) x 32 c of an accumulator into rows of out.
+// A warp turns 32 m (its TMEM lanes) x 16 c of an accumulator into rows of out.
 // The accumulator has c along its columns and memory has m contiguous: pairs of
-// c are packed to bf16 in registers, stmatrix transposes them into 2 KB of the
-// warp's own shared memory, and each lane moves four 16-byte pieces (8 m of one
+// c are packed to bf16 in registers, stmatrix transposes them into 1 KB of the
+// warp's own shared memory, and each lane moves two 16-byte pieces (8 m of one
 // c) to memory; 1 store for 8 elements, where storing the columns one by one
 // took 22 instructions an element and held the gradient of 128 experts'
 // weights at 1.3 TB/s. The residual comes in the same way backwards, read by
 // the lane that will write it. Piece v of row c lies at v ^ (c / 2 % 4): no bank
 // conflict in either direction.
-constexpr int kStageBytes = 32 * 64;
+constexpr int kChunk = 16;
+constexpr int kStageBytes = kChunk * 64;
+constexpr int kEpiWarps = 16;   // of the pair kernel
 
 struct WarpStage {
     uint32_t mat;       // shared address of this lane's row for ldmatrix / stmatrix, c group 0
@@ -204,12 +204,12 @@ struct WarpStage {
     }
 };
 
-// The staged 32 x 32 values to dst + c * ld (dst: this lane's piece of row lane / 4).
+// The staged 16 x 32 values to dst + c * ld (dst: this lane's piece of row lane / 4).
 __device__ __forceinline__ void copy_out(const WarpStage &w, uint16_t *dst, long long ld8, int rows)
 {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kChunk / 8; ++i) {
         if (8 * i < rows)
             *reinterpret_cast<uint4 *>(dst) = w.vec[i * 32];
         dst += ld8;
@@ -217,18 +217,18 @@ __device__ __forceinline__ void copy_out(const WarpStage &w, uint16_t *dst, long
     __syncwarp();
 }
 
-// 32 lanes x 32 columns of an accumulator; tmem_ld_wait() before v is used.
-__device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[2][16])
+// 32 lanes x 16 columns of an accumulator; tmem_ld_wait() before v is used.
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[2][8])
 {
     tmem_ld16(taddr, v[0]);
     tmem_ld16(taddr + (16u << 16), v[1]);
 }
 
-// Columns [0, n) of an accumulator, n <= 32, to rows c0 + [0, n) of m [m0, m0 + 32)
+// Columns [0, n) of an accumulator, n <= 16, to rows c0 + [0, n) of m [m0, m0 + 32)
 // cut at M. bias[i]: of m0 + 8 i + lane / 4. `loaded` runs between the residual's
 // loads and the first use of v.
 template <LinMode MODE, int ACT, class F>
-__device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][16],
+__device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][8],
                                             const float (&bias)[4], long long c0, int m0, int M,
                                             int n, int lane, const WarpStage &w, F loaded)
 {
@@ -236,21 +236,21 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][16],
     // rows this lane moves: c = lane / 4 + 8 i < n, none when its m lie past the end
     const int rows = m < M ? n - (lane >> 2) : 0;
     const long long at = (c0 + (lane >> 2)) * o.ld + m, ld8 = 8 * o.ld;
-    uint4 res[4];
+    uint4 res[kChunk / 8];
     if (MODE == LIN_FWD && o.residual) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kChunk / 8; ++i)
             if (8 * i < rows)
                 res[i] = *reinterpret_cast<const uint4 *>(o.residual + at + i * ld8);
     }
     loaded();
     if (MODE == LIN_FWD) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i >> 4][i & 15] += bias[(i >> 4) * 2 + ((i >> 1) & 1)];
+        for (int i = 0; i < 16; ++i)
+            v[i >> 3][i & 7] += bias[(i >> 3) * 2 + ((i >> 1) & 1)];
         if (o.z) {
 #pragma unroll
-            for (int ci = 0; ci < 4; ++ci) {
+            for (int ci = 0; ci < kChunk / 8; ++ci) {
                 uint32_t r[4];
 #pragma unroll
                 for (int mi = 0; mi < 4; ++mi) {
@@ -263,14 +263,14 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][16],
         }
         if (o.residual) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kChunk / 8; ++i)
                 if (8 * i < rows)
                     w.vec[i * 32] = res[i];
             __syncwarp();
         }
     }
 #pragma unroll
-    for (int ci = 0; ci < 4; ++ci) {
+    for (int ci = 0; ci < kChunk / 8; ++ci) {
         uint32_t r[4];
         if (MODE == LIN_FWD && o.residual)
             ldmatrix4_t(w.mat + ci * 512, r);
@@ -289,35 +289,36 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][16],
     copy_out(w, o.out + at, ld8, rows);
 }
 
-// A warp's part of a tile: columns h * 32 + [0, 32), and every 64 from there, below cn.
-// Two chunks' loads go out together where the registers allow it, and `release` runs
-// as soon as the last value has left the accumulator.
-template <LinMode MODE, int ACT, class R>
+// A warp's part of a tile: columns h * 16 + [0, 16), and every 16 NH from there, below
+// cn (NH warps share a lane quarter). Two chunks' loads go out together where the
+// registers allow it, and `release` runs as soon as the last value has left the
+// accumulator.
+template <LinMode MODE, int ACT, int NH, class R>
 __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
                                            const float (&bias)[4], long long c0, int m0, int M,
                                            int cn, int lane, const WarpStage &w, R release)
 {
-    constexpr int STEP = MODE == LIN_FWD ? 64 : 128;
-    const int first = h * 32;
+    constexpr int SKIP = kChunk * NH, STEP = MODE == LIN_FWD ? SKIP : 2 * SKIP;
+    const int first = h * kChunk;
     if (m0 >= M || first >= cn) {
         release();
         return;
     }
 #pragma unroll 1
     for (int c = first; c < cn; c += STEP) {
-        float v[2][16], v2[2][16];
+        float v[2][8], v2[2][8];
         load_acc(tb + c, v);
-        const bool two = MODE != LIN_FWD && c + 64 < cn;
+        const bool two = MODE != LIN_FWD && c + SKIP < cn;
         if (two)
-            load_acc(tb + c + 64, v2);
-        store_chunk<MODE, ACT>(o, v, bias, c0 + c, m0, M, min(32, cn - c), lane, w, [&] {
+            load_acc(tb + c + SKIP, v2);
+        store_chunk<MODE, ACT>(o, v, bias, c0 + c, m0, M, min(kChunk, cn - c), lane, w, [&] {
             tmem_ld_wait();
             if (c + STEP >= cn)
                 release();
         });
         if (two)
-            store_chunk<MODE, ACT>(o, v2, bias, c0 + c + 64, m0, M, min(32, cn - c - 64), lane, w,
-                                   [] {});
+            store_chunk<MODE, ACT>(o, v2, bias, c0 + c + SKIP, m0, M, min(kChunk, cn - c - SKIP), lane,
+                                   w, [] {});
     }
 }
 
@@ -326,7 +327,7 @@ __device__ __forceinline__ void store_zeros(const LinOut &o, int h, long long c0
                                             int lane)
 {
     const int m = m0 + (lane & 3) * 8;
-    for (int c = h * 8 + (lane >> 2); c < cn && m < M; c += 16)
+    for (int c = h * 8 + (lane >> 2); c < cn && m < M; c += 8 * (kEpiWarps / 4))
         *reinterpret_cast<uint4 *>(o.out + (c0 + c) * o.ld + m) = make_uint4(0, 0, 0, 0);
 }
 
@@ -373,12 +374,13 @@ __device__ __forceinline__ void load_bias(const LinOut &o, long long first, int 
 // columns alternate, so a tile's epilogue overlaps the next tile's main loop.
 //   warp 0   producer        warp 1   MMA issue (leader)
 //   warp 2   dW: zeroes the rows of a group's last block past its end
-//   warps 4-11  epilogue, two per TMEM lane quarter, alternating 32 columns
-constexpr int kPairThreads = 384;
+//   warps 4-19  epilogue, four per TMEM lane quarter, taking 16 columns in turn. With two
+//               per quarter 16384 x 256 -> 4096 took 45 us and 103 with gelu
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;
 constexpr int kPairABytes = 2 * kBoxBytes;
 constexpr int kRingBytes = 24 * kBoxBytes;
 constexpr int kPairBars = 768;
-constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + 8 * kStageBytes;
+constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + kEpiWarps * kStageBytes;
 
 // Stages of the ring for tiles of each class (class 0: up to 256 rows; 1: 128; 2:
 // 64): the smaller the tokens' part of a stage, the more stages fit. A stage's round
@@ -597,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(&tailbar[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 16);   // 8 epilogue warps of each CTA
+            mbar_init(&tempty[b], 2 * kEpiWarps);   // of both CTAs
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -830,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         mbar_arrive_remote(mapa_shared(smem_u32(&tempty[b]), 0));
                 };
                 if (MODE == LIN_DW && p.o.part) {
-                    for (int c = h * 32; c < cn && m0 < M; c += 64)
+                    for (int c = h * 32; c < cn && m0 < M; c += 32 * (kEpiWarps / 4))
                         store_part(p.o.part, p.o.ld, tb + c, none, c0 + c, m0 + lane, M,
                                    min(32, cn - c));
                     if (!none)
@@ -838,7 +840,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 } else if (none) {
                     store_zeros(p.o, h, c0, m0, M, cn, lane);
                 } else {
-                    store_tile<MODE, ACT>(p.o, tb, h, bias, c0, m0, M, cn, lane, ws, release);
+                    store_tile<MODE, ACT, kEpiWarps / 4>(p.o, tb, h, bias, c0, m0, M, cn, lane, ws,
+                                                         release);
                 }
             }
             return true;
@@ -1004,7 +1007,7 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         float bias[4];
         load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
         if (got)
-            store_tile<MODE, ACT>(p.o, tb, h, bias, c0, mq, M, cn, lane, ws, [] {});
+            store_tile<MODE, ACT, 2>(p.o, tb, h, bias, c0, mq, M, cn, lane, ws, [] {});
     } else {
         // partial sums [c][128 m] over the ring, which every copy and MMA has left
         float *mine = reinterpret_cast<float *>(smem);
