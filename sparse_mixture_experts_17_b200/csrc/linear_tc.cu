@@ -224,25 +224,36 @@ __device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[2][8])
     tmem_ld16(taddr + (16u << 16), v[1]);
 }
 
+// This lane's pieces of the residual's rows c0 + [0, n), n <= 16 (see store_chunk).
+template <LinMode MODE>
+__device__ __forceinline__ void load_residual(const LinOut &o, long long c0, int m0, int M, int n,
+                                              int lane, uint4 (&res)[kChunk / 8])
+{
+    if (MODE != LIN_FWD || !o.residual)
+        return;
+    const int m = m0 + (lane & 3) * 8, rows = m < M ? n - (lane >> 2) : 0;
+    const uint16_t *src = o.residual + (c0 + (lane >> 2)) * o.ld + m;
+#pragma unroll
+    for (int i = 0; i < kChunk / 8; ++i) {
+        if (8 * i < rows)
+            res[i] = *reinterpret_cast<const uint4 *>(src);
+        src += 8 * o.ld;
+    }
+}
+
 // Columns [0, n) of an accumulator, n <= 16, to rows c0 + [0, n) of m [m0, m0 + 32)
-// cut at M. bias[i]: of m0 + 8 i + lane / 4. `loaded` runs between the residual's
-// loads and the first use of v.
+// cut at M. bias[i]: of m0 + 8 i + lane / 4; res: this lane's pieces of the residual.
+// `loaded` runs before the first use of v.
 template <LinMode MODE, int ACT, class F>
 __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][8],
-                                            const float (&bias)[4], long long c0, int m0, int M,
-                                            int n, int lane, const WarpStage &w, F loaded)
+                                            const float (&bias)[4], const uint4 (&res)[kChunk / 8],
+                                            long long c0, int m0, int M, int n, int lane,
+                                            const WarpStage &w, F loaded)
 {
     const int m = m0 + (lane & 3) * 8;
     // rows this lane moves: c = lane / 4 + 8 i < n, none when its m lie past the end
     const int rows = m < M ? n - (lane >> 2) : 0;
     const long long at = (c0 + (lane >> 2)) * o.ld + m, ld8 = 8 * o.ld;
-    uint4 res[kChunk / 8];
-    if (MODE == LIN_FWD && o.residual) {
-#pragma unroll
-        for (int i = 0; i < kChunk / 8; ++i)
-            if (8 * i < rows)
-                res[i] = *reinterpret_cast<const uint4 *>(o.residual + at + i * ld8);
-    }
     loaded();
     if (MODE == LIN_FWD) {
 #pragma unroll
@@ -292,11 +303,12 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][8],
 // A warp's part of a tile: columns h * 16 + [0, 16), and every 16 NH from there, below
 // cn (NH warps share a lane quarter). Two chunks' loads go out together where the
 // registers allow it, and `release` runs as soon as the last value has left the
-// accumulator.
+// accumulator. res: of the first chunk; each next one's goes out a chunk ahead.
 template <LinMode MODE, int ACT, int NH, class R>
 __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
-                                           const float (&bias)[4], long long c0, int m0, int M,
-                                           int cn, int lane, const WarpStage &w, R release)
+                                           const float (&bias)[4], uint4 (&res)[kChunk / 8],
+                                           long long c0, int m0, int M, int cn, int lane,
+                                           const WarpStage &w, R release)
 {
     constexpr int SKIP = kChunk * NH, STEP = MODE == LIN_FWD ? SKIP : 2 * SKIP;
     const int first = h * kChunk;
@@ -307,18 +319,23 @@ __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
 #pragma unroll 1
     for (int c = first; c < cn; c += STEP) {
         float v[2][8], v2[2][8];
+        uint4 next[kChunk / 8];
         load_acc(tb + c, v);
         const bool two = MODE != LIN_FWD && c + SKIP < cn;
         if (two)
             load_acc(tb + c + SKIP, v2);
-        store_chunk<MODE, ACT>(o, v, bias, c0 + c, m0, M, min(kChunk, cn - c), lane, w, [&] {
+        load_residual<MODE>(o, c0 + c + STEP, m0, M, min(kChunk, cn - c - STEP), lane, next);
+        store_chunk<MODE, ACT>(o, v, bias, res, c0 + c, m0, M, min(kChunk, cn - c), lane, w, [&] {
             tmem_ld_wait();
             if (c + STEP >= cn)
                 release();
         });
         if (two)
-            store_chunk<MODE, ACT>(o, v2, bias, c0 + c + SKIP, m0, M, min(kChunk, cn - c - SKIP), lane,
-                                   w, [] {});
+            store_chunk<MODE, ACT>(o, v2, bias, res, c0 + c + SKIP, m0, M, min(kChunk, cn - c - SKIP),
+                                   lane, w, [] {});
+#pragma unroll
+        for (int i = 0; i < kChunk / 8; ++i)
+            res[i] = next[i];
     }
 }
 
@@ -818,6 +835,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int cn = part ? a.cn2 : a.cn;
                 const long long c0 = c00 + a.c0 + (part ? a.cn : 0);
                 const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
+                uint4 res[kChunk / 8];
+                load_residual<MODE>(p.o, c0 + h * kChunk, m0, M, min(kChunk, cn - h * kChunk), lane, res);
                 if (!none) {
                     if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
                         return false;
@@ -840,8 +859,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 } else if (none) {
                     store_zeros(p.o, h, c0, m0, M, cn, lane);
                 } else {
-                    store_tile<MODE, ACT, kEpiWarps / 4>(p.o, tb, h, bias, c0, m0, M, cn, lane, ws,
-                                                         release);
+                    store_tile<MODE, ACT, kEpiWarps / 4>(p.o, tb, h, bias, res, c0, m0, M, cn, lane,
+                                                         ws, release);
                 }
             }
             return true;
@@ -995,19 +1014,22 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
     __syncwarp();
 
     // ---------------- epilogue: all eight warps, two per TMEM lane quarter
-    const bool got = __all_sync(kFullMask, mbar_wait(done, 0, abort_flag, p.status));
-    tc_fence_after();
-    const int q = warp & 3, h = warp >> 2;
+    const int q = warp & 3, h = warp >> 2, mq = m0 + q * 32;
     const int M = MODE == LIN_FWD ? p.d_out : p.d_in;
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    float bias[4];
+    uint4 res[kChunk / 8];
+    if (p.S == 1) {
+        load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
+        load_residual<MODE>(p.o, c0 + h * kChunk, mq, M, min(kChunk, cn - h * kChunk), lane, res);
+    }
+    const bool got = __all_sync(kFullMask, mbar_wait(done, 0, abort_flag, p.status));
+    tc_fence_after();
     if (p.S == 1) {
         // the ring, which every copy and MMA has left, holds the rows on their way out
         const WarpStage ws(smem + warp * kStageBytes, lane);
-        const int mq = m0 + q * 32;
-        float bias[4];
-        load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
         if (got)
-            store_tile<MODE, ACT, 2>(p.o, tb, h, bias, c0, mq, M, cn, lane, ws, [] {});
+            store_tile<MODE, ACT, 2>(p.o, tb, h, bias, res, c0, mq, M, cn, lane, ws, [] {});
     } else {
         // partial sums [c][128 m] over the ring, which every copy and MMA has left
         float *mine = reinterpret_cast<float *>(smem);
