@@ -308,10 +308,16 @@ int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.d_out = s.d_out;
     p.E = s.E;
     p.status = status;
+    // dz (if any) has completed when the bias sums start, and those when dx starts, ...:
+    // each of the three lets its successor start only after its own wait, and none
+    // reads what another writes. (4096 x 2048 -> 4096: dx and dW are 128 tiles each for
+    // 74 pairs of SMs, and two rounds of one leave 20 pairs to the other.)
+    p.late = dbias != nullptr;
     if (dx) {
         p.out = dx;
         if ((rc = launch_linear(LIN_DX, p, st)))
             return rc;
+        p.late = true;
     }
     if (dW) {
         p.out = dW;

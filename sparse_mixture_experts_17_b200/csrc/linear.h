@@ -25,6 +25,11 @@ struct LinArgs {
     const int32_t *offsets;       // NULL: one group of all rows
     int rows, d_in, d_out, E, act;
     int splits;                   // LIN_DW
+    // The product needs nothing of the kernel launched just before it, and what it does
+    // need had completed before that one let its successor start: it starts at once,
+    // beside that kernel's last CTAs, and waits for it only before it ends (so that
+    // whatever waits for this product has waited for both).
+    bool late;
     uint32_t *status;
 };
 

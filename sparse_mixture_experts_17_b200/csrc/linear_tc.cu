@@ -474,6 +474,7 @@ struct PairArgs {
     int splits;      // LIN_DW
     Divisor by_m, by_c, by_split;   // m_tiles, c_tiles, splits
     bool a_wide, b_wide;   // MN-major operands: two boxes in one copy
+    bool late;       // see LinArgs
     LinOut o;
     uint32_t *status;
 };
@@ -629,7 +630,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
-    pdl_wait();
+    if (!p.late)
+        pdl_wait();
     pdl_trigger();
     // items of one group: token tiles; LIN_DW needs the groups' rows only
     build_groups<true>(G, p.offsets, p.E, p.rows, WIDE ? 2 * kTileC : kTileC, p.status);
@@ -879,6 +881,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
     }
+    if (p.late)
+        pdl_wait();
 }
 
 // ---------------------------------------------------------------- split kernel
@@ -904,6 +908,7 @@ struct SplitArgs {
     int S;
     int kblocks;
     bool a_wide;
+    bool late;       // see LinArgs
     LinOut o;
     uint32_t *status;
 };
@@ -944,7 +949,8 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         tmem_alloc(tmem_slot, BC);
         tmem_relinquish();
     }
-    pdl_wait();
+    if (!p.late)
+        pdl_wait();
     pdl_trigger();
     const int item = blockIdx.y;
     int e = 0, c0 = item * BC, cn = min(BC, p.rows - c0);
@@ -967,6 +973,8 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
     if (!any) {
         if (warp == 1)
             tmem_dealloc(tmem_base, BC);
+        if (p.late)
+            pdl_wait();
         return;
     }
 
@@ -1098,6 +1106,8 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, BC);
     }
+    if (p.late)
+        pdl_wait();
 }
 
 // dW = bf16(sum over the splits, in order).
@@ -1241,6 +1251,7 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
     p.by_split.set(p.splits);
     p.a_wide = a_wide;
     p.b_wide = b_wide;
+    p.late = a.late;
     p.o = out_of(MODE, a);
     p.status = a.status;
     const long long tiles =
@@ -1280,6 +1291,7 @@ int launch_split(const LinArgs &a, int S, cudaStream_t st)
     p.d_out = a.d_out;
     p.S = S;
     p.a_wide = a_wide;
+    p.late = a.late;
     p.kblocks = ceil_div(MODE == LIN_FWD ? a.d_in : a.d_out, kBox);
     p.o = out_of(MODE, a);
     p.status = a.status;

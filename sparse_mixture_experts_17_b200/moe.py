@@ -519,14 +519,18 @@ _KINDS = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
 def _tensor_list(tensors, name):
     """(pointers, element counts, MOE_TYPE_*) of fp32 / bf16 tensors on one device, as host
     arrays."""
-    ptrs, _ = _args(*[(t, None, None, name) for t in tensors])
-    types = []
-    for i, t in enumerate(tensors):
-        if t is None or t.dtype not in _KINDS:
-            raise TypeError(f"{name}[{i}]: expected float32 or bfloat16, got "
-                            f"{None if t is None else t.dtype}")
-        types.append(_KINDS[t.dtype])
-    return array("Q", ptrs), array("q", [t.numel() for t in tensors]), array("i", types)
+    Tensor = torch.Tensor
+    if all([type(t) is Tensor or isinstance(t, Tensor) for t in tensors]):   # the usual case, in few steps
+        devs = set(map(Tensor.get_device, tensors))
+        types = [_KINDS.get(t.dtype) for t in tensors]
+        if len(devs) <= 1 and -1 not in devs and None not in types and \
+                all(map(Tensor.is_contiguous, tensors)):
+            return (array("Q", map(Tensor.data_ptr, tensors)), array("q", map(Tensor.numel, tensors)),
+                    array("i", types))
+    _args(*[(t, None, None, f"{name}[{i}]") for i, t in enumerate(tensors)])
+    bad = [(i, t) for i, t in enumerate(tensors) if t is None or t.dtype not in _KINDS][0]
+    raise TypeError(f"{name}[{bad[0]}]: expected float32 or bfloat16, got "
+                    f"{None if bad[1] is None else bad[1].dtype}")
 
 
 def _address(a):
