@@ -905,7 +905,7 @@ struct SplitCfg {
 struct SplitArgs {
     const int32_t *offsets;
     int E, rows, d_in, d_out;
-    int S;
+    int S, log_s;
     int kblocks;
     bool a_wide;
     bool late;       // see LinArgs
@@ -1059,38 +1059,54 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         }
         __syncwarp();
         cluster_sync_all();
-        // each CTA finishes 128 / S of the m of every token
-        const int mw = 128 / p.S;
+        // each CTA finishes 128 / S of the m of every token, a thread four of them (S is a
+        // power of two, and all sizes are multiples of 8)
+        const int quads = 5 - p.log_s;   // log2 of (128 / S) / 4
         uint32_t peer[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             peer[r] = r < p.S ? mapa_shared(smem_u32(mine), r) : 0u;
         if (got)
-            for (int i = threadIdx.x; i < cn * mw; i += 256) {
-                const int c = i / mw, ml = rank * mw + i % mw, m = m0 + ml;
+            for (int i = threadIdx.x; i < cn << quads; i += 256) {
+                const int c = i >> quads, ml = (rank << (quads + 2)) + (i & ((1 << quads) - 1)) * 4;
+                const int m = m0 + ml;
                 if (m >= M)
                     continue;
-                float f = 0.f;
+                float4 part[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
-                    if (r < p.S) {
-                        float v;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(v)
+                    if (r < p.S)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(part[r].x), "=f"(part[r].y), "=f"(part[r].z), "=f"(part[r].w)
                                      : "r"(peer[r] + (uint32_t)(c * 128 + ml) * 4u));
-                        f += v;
-                    }
                 const long long at = (long long)(c0 + c) * p.o.ld + m;
+                uint2 res = make_uint2(0, 0);
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (MODE == LIN_FWD) {
-                    if (p.o.bias)
-                        f += p.o.bias[(long long)e * p.d_out + m];
-                    if (p.o.z)
-                        p.o.z[at] = (uint16_t)pack_bf16x2(f, 0.f);
-                    f = act_f<ACT>(f);
                     if (p.o.residual)
-                        f += __uint_as_float((uint32_t)p.o.residual[at] << 16);
+                        res = *reinterpret_cast<const uint2 *>(p.o.residual + at);
+                    if (p.o.bias)
+                        f = *reinterpret_cast<const float4 *>(p.o.bias + (long long)e * p.d_out + m);
                 }
-                p.o.out[at] = (uint16_t)pack_bf16x2(f, 0.f);
+                float4 sum = part[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < p.S)
+                        sum.x += part[r].x, sum.y += part[r].y, sum.z += part[r].z, sum.w += part[r].w;
+                if (MODE == LIN_FWD) {
+                    sum.x += f.x, sum.y += f.y, sum.z += f.z, sum.w += f.w;
+                    if (p.o.z)
+                        *reinterpret_cast<uint2 *>(p.o.z + at) =
+                            make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                    sum.x = act_f<ACT>(sum.x), sum.y = act_f<ACT>(sum.y);
+                    sum.z = act_f<ACT>(sum.z), sum.w = act_f<ACT>(sum.w);
+                    if (p.o.residual) {
+                        sum.x += bf16lo(res.x), sum.y += bf16hi(res.x);
+                        sum.z += bf16lo(res.y), sum.w += bf16hi(res.y);
+                    }
+                }
+                *reinterpret_cast<uint2 *>(p.o.out + at) =
+                    make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
             }
         __syncwarp();
         cluster_sync_all();   // no CTA leaves while another reads its sums
@@ -1290,6 +1306,8 @@ int launch_split(const LinArgs &a, int S, cudaStream_t st)
     p.d_in = a.d_in;
     p.d_out = a.d_out;
     p.S = S;
+    while (1 << p.log_s < S)
+        ++p.log_s;
     p.a_wide = a_wide;
     p.late = a.late;
     p.kblocks = ceil_div(MODE == LIN_FWD ? a.d_in : a.d_out, kBox);
@@ -1337,16 +1355,25 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
             return launch_pair<MODE, ACT, true>(a, st);
         return launch_pair<MODE, ACT>(a, st);
     }
-    // tiles no wider than the groups; narrower where that leaves half the SMs without
-    // one (the weights are then read more than once, but from L2)
-    int bc = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
-    const auto tiles_of = [&](int b) { return (long long)groups * ceil_div(avg, b) * ceil_div(M, 128); };
-    while (bc > 32 && tiles_of(bc) * 2 <= sms)
+    // Tiles as wide as the groups (half as much again where those are ragged, so that few
+    // are cut in two: 1024 x 1024 -> 1024 in 32 groups 15.2 us against 19.8); narrower
+    // where that leaves half the SMs without one (300 x 1024 -> 1024: 6.7 with 32, 9.3 with
+    // 128; the weights are then read more than once, but from L2).
+    const int kb = ceil_div(K, kBox), need = a.offsets ? avg + avg / 2 : avg;
+    int bc = need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : 256;
+    const auto tiles_of = [&](int b) {
+        const long long items = a.offsets ? a.rows / b + groups : ceil_div(a.rows, b);
+        return items * ceil_div(M, 128);
+    };
+    while (bc > (kb >= 32 ? 64 : 32) && tiles_of(bc) * 2 <= sms)
         bc /= 2;
     const long long tiles = tiles_of(bc);
-    // CTAs that split K: enough to fill the SMs, each with four K stages or more
+    // CTAs that split K: enough to fill the SMs, each with eight K stages or more, four for
+    // few rows, whose sums are joined sooner (one row, 2048 -> 2048: 4.6 us with four, 5.5
+    // with eight, 11.5 unsplit; 1000 x 512 -> 512: 6.2 with four, 4.9 unsplit)
+    const int stages = avg <= 16 ? 4 : 8;
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= (bc == 256 ? sms : 2 * sms) && ceil_div(K, kBox) >= 2 * S * 4)
+    while (S < 8 && tiles * S * 2 <= (bc == 256 ? sms : 2 * sms) && kb >= 2 * S * stages)
         S *= 2;
     switch (bc) {
     case 32: return launch_split<MODE, ACT, 32>(a, S, st);
