@@ -399,22 +399,21 @@ def _on_one_device(**tensors):
         raise ValueError("tensors on different devices: " + ", ".join(
             f"{n} on {t.device}" for n, t in tensors.items()
             if isinstance(t, torch.Tensor) and t.is_cuda))
-    return torch.cuda.device(devs.pop()) if devs else _HERE
+    return torch.cuda.device(devs.pop()) if devs else contextlib.nullcontext()
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _args(*specs):
-    """Checked pointers of tensors given as (tensor, dtype or None, shape or None, name), and the
-    context of _on_one_device. An expected leading axis of 1 may be missing."""
+def _args(names, dtypes, shapes, tensors):
+    """Checked pointers of tensors (None stays None), and the context of _on_one_device. dtypes and
+    shapes: None where any will do; an int shape is a least number of elements; an expected
+    leading axis of 1 may be missing."""
     ptrs, here, Tensor = [], -1, torch.Tensor
-    for t, dtype, shape, _ in specs:   # what nearly every call passes, with few steps
+    for t, dtype, shape in zip(tensors, dtypes, shapes):   # what nearly every call passes, in few steps
         if t is None:
             ptrs.append(None)
             continue
         if not (isinstance(t, Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and
-                (shape is None or t.shape == shape) and t.is_contiguous()):
+                (shape is None or t.shape == shape or (type(shape) is int and t.numel() >= shape)) and
+                t.is_contiguous()):
             break
         if here < 0:
             here = torch.cuda.current_device()
@@ -422,21 +421,29 @@ def _args(*specs):
             break
         ptrs.append(t.data_ptr())
     else:
-        return ptrs, _HERE
-    for t, _, shape, name in specs:
-        if shape is not None and isinstance(t, torch.Tensor) and t.shape != shape and (
-                shape[0] != 1 or t.shape != shape[1:]):
+        return ptrs, None
+    for name, t, shape in zip(names, tensors, shapes):
+        if shape is None or t is None or not isinstance(t, Tensor):
+            continue
+        if type(shape) is int:
+            if t.numel() < shape:
+                raise ValueError(f"{name}: expected at least {shape} elements, got {t.numel()}")
+        elif t.shape != shape and (shape[0] != 1 or t.shape != shape[1:]):
             raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    ptrs, named = [], {}
-    for i, (t, dtype, _, name) in enumerate(specs):
-        ptrs.append(_ptr(t, dtype, name))
-        named[f"{name}[{i}]" if name in named else name] = t
-    return ptrs, _on_one_device(**named)
+    ptrs = [_ptr(t, dtype, name) for name, dtype, t in zip(names, dtypes, tensors)]
+    return ptrs, _on_one_device(**dict(zip(names, tensors)))
 
 
-def _at_least(t, n, name):
-    if t is not None and isinstance(t, torch.Tensor) and t.numel() < n:
-        raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+def _call(name, on_device, *args, stream):
+    """Calls an entry point, its stream last, with the tensors' device current (on_device None: it is)."""
+    f = getattr(lib(), name)
+    if on_device is None:
+        rc = f(*args, _stream(stream))
+    else:
+        with on_device:
+            rc = f(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(name, rc, status_string(rc))
 
 
 def moe_linear_workspace_size(shape: moe_linear_t) -> int:
@@ -451,66 +458,60 @@ def alloc_linear_workspace(shape: moe_linear_t, device="cuda") -> torch.Tensor:
     return torch.empty(moe_linear_workspace_size(shape), dtype=torch.uint8, device=device)
 
 
+_LINEAR_FORWARD = (("x", "expert_offsets", "W", "bias", "residual", "y", "z", "status"),
+                   (BF16, I32, BF16, F32, BF16, BF16, BF16, U32))
+
+
 def moe_linear_forward(shape, x, expert_offsets, W, bias, residual, y, z=None, status=None,
                        stream=None):
     """y = act(x W_e^T + b_e) + residual over the groups of expert_offsets (None: dense, E = 1);
     z (optional) receives the pre-activation. With E = 1, W and bias may lack the expert axis."""
     R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
-    _at_least(expert_offsets, E + 1, "expert_offsets")
-    _at_least(status, 1, "status")
-    ptrs, on_device = _args(
-        (x, BF16, (R, di), "x"), (expert_offsets, I32, None, "expert_offsets"),
-        (W, BF16, (E, do, di), "W"), (bias, F32, (E, do), "bias"),
-        (residual, BF16, (R, do), "residual"), (y, BF16, (R, do), "y"), (z, BF16, (R, do), "z"),
-        (status, U32, None, "status"))
-    with on_device:
-        _check("moe_linear_forward",
-               lib().moe_linear_forward(ctypes.byref(shape), *ptrs, _stream(stream)))
+    rows = (R, do)
+    ptrs, on_device = _args(*_LINEAR_FORWARD, ((R, di), E + 1, (E, do, di), (E, do), rows, rows, rows, 1),
+                            (x, expert_offsets, W, bias, residual, y, z, status))
+    _call("moe_linear_forward", on_device, ctypes.byref(shape), *ptrs, stream=stream)
     return y
+
+
+_LINEAR_BACKWARD = (("x", "expert_offsets", "W", "z", "dy", "dx", "dW", "dbias", "status", "ws"),
+                    (BF16, I32, BF16, BF16, BF16, BF16, BF16, F32, U32, None))
 
 
 def moe_linear_backward(shape, x, expert_offsets, W, z, dy, dx, dW, dbias, status, ws, stream=None):
     """Gradients of sum(y * dy): dx, dW and dbias (each may be None)."""
     R, di, do, E = shape.rows, shape.d_in, shape.d_out, shape.E
-    _at_least(expert_offsets, E + 1, "expert_offsets")
-    _at_least(status, 1, "status")
-    ptrs, on_device = _args(
-        (x, BF16, (R, di), "x"), (expert_offsets, I32, None, "expert_offsets"),
-        (W, BF16, (E, do, di), "W"), (z, BF16, (R, do), "z"), (dy, BF16, (R, do), "dy"),
-        (dx, BF16, (R, di), "dx"), (dW, BF16, (E, do, di), "dW"), (dbias, F32, (E, do), "dbias"),
-        (status, U32, None, "status"), (ws, None, None, "ws"))
-    with on_device:
-        _check("moe_linear_backward", lib().moe_linear_backward(
-            ctypes.byref(shape), *ptrs, _nbytes(ws), _stream(stream)))
+    ptrs, on_device = _args(*_LINEAR_BACKWARD,
+                            ((R, di), E + 1, (E, do, di), (R, do), (R, do), (R, di), (E, do, di), (E, do), 1, None),
+                            (x, expert_offsets, W, z, dy, dx, dW, dbias, status, ws))
+    _call("moe_linear_backward", on_device, ctypes.byref(shape), *ptrs, _nbytes(ws), stream=stream)
+
+
+_COMBINE_ROWS = (("y_perm", "slot_pos", "topk_w", "residual", "out", "status"),
+                 (BF16, I32, F32, BF16, BF16, U32))
 
 
 def moe_combine_rows(shape, y_perm, slot_pos, topk_w, residual, out, status=None, stream=None):
     """out[t] = residual[t] + sum_j w[t,j] y_perm[slot_pos[t,j]], bf16 rows (topk_w None: all 1)."""
     T, d, k = shape.T, shape.d, shape.k
-    _at_least(status, 1, "status")
-    ptrs, on_device = _args(
-        (y_perm, BF16, (T * k, d), "y_perm"), (slot_pos, I32, (T, k), "slot_pos"),
-        (topk_w, F32, (T, k), "topk_w"), (residual, BF16, (T, d), "residual"),
-        (out, BF16, (T, d), "out"), (status, U32, None, "status"))
-    with on_device:
-        _check("moe_combine_rows",
-               lib().moe_combine_rows(ctypes.byref(shape), *ptrs, _stream(stream)))
+    ptrs, on_device = _args(*_COMBINE_ROWS, ((T * k, d), (T, k), (T, k), (T, d), (T, d), 1),
+                            (y_perm, slot_pos, topk_w, residual, out, status))
+    _call("moe_combine_rows", on_device, ctypes.byref(shape), *ptrs, stream=stream)
     return out
+
+
+_COMBINE_ROWS_BACKWARD = (("dout", "y_perm", "slot_pos", "topk_w", "dy_perm", "dtopk_w", "status"),
+                          (BF16, BF16, I32, F32, BF16, F32, U32))
 
 
 def moe_combine_rows_backward(shape, dout, y_perm, slot_pos, topk_w, dy_perm, dtopk_w, status=None,
                               stream=None):
     """Gradients of sum(out * dout) of moe_combine_rows: dy_perm and dtopk_w (either may be None)."""
     T, d, k = shape.T, shape.d, shape.k
-    _at_least(status, 1, "status")
-    ptrs, on_device = _args(
-        (dout, BF16, (T, d), "dout"), (y_perm, BF16, (T * k, d), "y_perm"),
-        (slot_pos, I32, (T, k), "slot_pos"), (topk_w, F32, (T, k), "topk_w"),
-        (dy_perm, BF16, (T * k, d), "dy_perm"), (dtopk_w, F32, (T, k), "dtopk_w"),
-        (status, U32, None, "status"))
-    with on_device:
-        _check("moe_combine_rows_backward",
-               lib().moe_combine_rows_backward(ctypes.byref(shape), *ptrs, _stream(stream)))
+    ptrs, on_device = _args(*_COMBINE_ROWS_BACKWARD,
+                            ((T, d), (T * k, d), (T, k), (T, k), (T * k, d), (T, k), 1),
+                            (dout, y_perm, slot_pos, topk_w, dy_perm, dtopk_w, status))
+    _call("moe_combine_rows_backward", on_device, ctypes.byref(shape), *ptrs, stream=stream)
 
 
 _KINDS = {F32: MOE_TYPE_F32, BF16: MOE_TYPE_BF16}
@@ -527,7 +528,8 @@ def _tensor_list(tensors, name):
                 all(map(Tensor.is_contiguous, tensors)):
             return (array("Q", map(Tensor.data_ptr, tensors)), array("q", map(Tensor.numel, tensors)),
                     array("i", types))
-    _args(*[(t, None, None, f"{name}[{i}]") for i, t in enumerate(tensors)])
+    n = len(tensors)
+    _args([f"{name}[{i}]" for i in range(n)], [None] * n, [None] * n, tensors)
     bad = [(i, t) for i, t in enumerate(tensors) if t is None or t.dtype not in _KINDS][0]
     raise TypeError(f"{name}[{bad[0]}]: expected float32 or bfloat16, got "
                     f"{None if bad[1] is None else bad[1].dtype}")
@@ -543,19 +545,17 @@ def alloc_grad_workspace(grads=(), device="cuda") -> torch.Tensor:
     return torch.empty(MOE_GRAD_WS_BYTES, dtype=torch.uint8, device=dev)
 
 
+_GRADS = (("norm", "status", "ws", "grads", "outs"), (F32, U32, None, None, None), (1, 1, None, None, None))
+
+
 def moe_grad_norm(grads, norm, status=None, ws=None, stream=None):
     """norm[0] = the global 2-norm of a list of fp32 / bf16 tensors."""
     grads = list(grads)
     ptrs, numel, types = _tensor_list(grads, "grads")
-    _at_least(norm, 1, "norm")
-    _at_least(status, 1, "status")
-    (norm_p, status_p, ws_p, *_), on_device = _args(
-        (norm, F32, None, "norm"), (status, U32, None, "status"), (ws, None, None, "ws"),
-        *((t, None, None, "grads") for t in grads[:1]))
-    with on_device:
-        _check("moe_grad_norm", lib().moe_grad_norm(
-            len(grads), _address(ptrs), _address(numel), _address(types), norm_p, status_p, ws_p,
-            _nbytes(ws), _stream(stream)))
+    (norm_p, status_p, ws_p, _, _), on_device = _args(
+        *_GRADS, (norm, status, ws, grads[0] if grads else None, None))
+    _call("moe_grad_norm", on_device, len(grads), _address(ptrs), _address(numel), _address(types),
+          norm_p, status_p, ws_p, _nbytes(ws), stream=stream)
     return norm
 
 
@@ -564,25 +564,19 @@ def moe_clip_grads(grads, max_norm, norm, outs=None, status=None, ws=None, strea
     in place, or into `outs`."""
     grads = list(grads)
     ptrs, numel, types = _tensor_list(grads, "grads")
-    optrs, firsts = None, grads[:1]
+    optrs, first = None, None
     if outs is not None:
         outs = list(outs)
         if len(outs) != len(grads):
             raise ValueError(f"outs: expected {len(grads)} tensors, got {len(outs)}")
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if g.dtype != o.dtype or g.numel() != o.numel():
-                raise ValueError(f"outs[{i}]: must match grads[{i}] in type and size")
-        optrs, _, _ = _tensor_list(outs, "outs")
-        firsts = firsts + outs[:1]
-    _at_least(norm, 1, "norm")
-    _at_least(status, 1, "status")
-    (norm_p, status_p, ws_p, *_), on_device = _args(
-        (norm, F32, None, "norm"), (status, U32, None, "status"), (ws, None, None, "ws"),
-        *((t, None, None, "grads / outs") for t in firsts))
-    with on_device:
-        _check("moe_clip_grads", lib().moe_clip_grads(
-            len(grads), _address(ptrs), _address(optrs), _address(numel), _address(types),
-            float(max_norm), norm_p, status_p, ws_p, _nbytes(ws), _stream(stream)))
+        optrs, onumel, otypes = _tensor_list(outs, "outs")
+        if onumel != numel or otypes != types:
+            raise ValueError("outs: must match grads in types and sizes")
+        first = outs[0] if outs else None
+    (norm_p, status_p, ws_p, _, _), on_device = _args(
+        *_GRADS, (norm, status, ws, grads[0] if grads else None, first))
+    _call("moe_clip_grads", on_device, len(grads), _address(ptrs), _address(optrs), _address(numel),
+          _address(types), float(max_norm), norm_p, status_p, ws_p, _nbytes(ws), stream=stream)
     return norm
 
 
