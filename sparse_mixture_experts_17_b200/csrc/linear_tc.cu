@@ -339,12 +339,12 @@ __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
     }
 }
 
-// Zeros in place of a tile: the gradient of an empty group's weights.
-__device__ __forceinline__ void store_zeros(const LinOut &o, int h, long long c0, int m0, int M, int cn,
+// Zeros in place of a tile: the gradient of an empty group's weights. Rows of 256 bytes.
+__device__ __forceinline__ void store_zeros(const LinOut &o, int warp, long long c0, int mt, int M, int cn,
                                             int lane)
 {
-    const int m = m0 + (lane & 3) * 8;
-    for (int c = h * 8 + (lane >> 2); c < cn && m < M; c += 8 * (kEpiWarps / 4))
+    const int m = mt + (lane & 15) * 8;
+    for (int c = 2 * warp + (lane >> 4); c < cn && m < M; c += 2 * kEpiWarps)
         *reinterpret_cast<uint4 *>(o.out + (c0 + c) * o.ld + m) = make_uint4(0, 0, 0, 0);
 }
 
@@ -859,7 +859,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (!none)
                         release();
                 } else if (none) {
-                    store_zeros(p.o, h, c0, m0, M, cn, lane);
+                    store_zeros(p.o, warp - 4, c0, a.m0 + 128 * (int)rank, M, cn, lane);
                 } else {
                     store_tile<MODE, ACT, kEpiWarps / 4>(p.o, tb, h, bias, res, c0, m0, M, cn, lane,
                                                          ws, release);
