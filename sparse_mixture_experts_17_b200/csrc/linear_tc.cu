@@ -416,37 +416,35 @@ __host__ __device__ constexpr int ring_bar(int c) { return c == 0 ? 0 : c == 1 ?
 constexpr int kRingBars = 27;
 
 // A role's place in the ring: its stage's barrier (its index in full and empty), byte
-// offset and the parity of the stage's current use. Kept by steps, not by division:
-// the producer and the MMA issue are one thread each, and what they spend on a stage
-// is not hidden (divisions by a stage count of 6, 8 or 9 cost 8% of 16384 x 14336 -> 4096).
+// offset and the parity of the stage's current use. Kept by steps, not by division, and
+// with the class's numbers at hand: the producer and the MMA issue are one thread each,
+// and what they spend on a stage is not hidden. Divisions by a stage count of 6, 8 or 9
+// cost 8% of 16384 x 14336 -> 4096, and numbers chosen by class at every step 57% of
+// 73 x 14336 -> 18944 (141 us against 89).
 struct Ring {
     int cls, bar, at;
     uint32_t phase;
     bool used;
+    int first, end, bytes;
     __device__ __forceinline__ explicit Ring(int c)
-        : cls(c), bar(ring_bar(c)), at(0), phase(0), used(false)
+        : cls(c), bar(ring_bar(c)), at(0), phase(0), used(false), first(ring_bar(c)),
+          end(ring_bar(c) + ring_stages(c)), bytes(ring_stage_bytes(c))
     {
     }
     __device__ __forceinline__ void next()
     {
         used = true;
         ++bar;
-        at += ring_stage_bytes(cls);
-        if (bar == ring_bar(cls) + ring_stages(cls)) {
-            bar = ring_bar(cls);
+        at += bytes;
+        if (bar == end) {
+            bar = first;
             at = 0;
             phase ^= 1u;
         }
     }
     // the stage before this one
-    __device__ __forceinline__ int last() const
-    {
-        return bar == ring_bar(cls) ? bar + ring_stages(cls) - 1 : bar - 1;
-    }
-    __device__ __forceinline__ uint32_t last_phase() const
-    {
-        return bar == ring_bar(cls) ? phase ^ 1u : phase;
-    }
+    __device__ __forceinline__ int last() const { return bar == first ? end - 1 : bar - 1; }
+    __device__ __forceinline__ uint32_t last_phase() const { return bar == first ? phase ^ 1u : phase; }
 };
 static_assert(6 * ring_stage_bytes(0) <= kRingBytes && 8 * ring_stage_bytes(1) <= kRingBytes &&
                   9 * ring_stage_bytes(2) <= kRingBytes && 4 * ring_stage_bytes(3) <= kRingBytes,
@@ -786,9 +784,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const bool last = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
                     if (last && !mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status))
                         return false;
-                    if (!wait_full(ring))
+                    if (!mbar_wait(&full[ring.bar], ring.phase, abort_flag, p.status))
                         return false;
-                    mma(d, idesc, ring, kPairABytes, kb != 0, last ? a.tail : kBox);
+                    tc_fence_after();
+                    const uint64_t da = op_desc<A_MN>(smem0 + ring.at, 0);
+                    const uint64_t db = op_desc<B_MN>(smem0 + ring.at + kPairABytes, 0);
+#pragma unroll
+                    for (int kk = 0; kk < kBox / 16; ++kk)
+                        if (!last || kk * 16 < a.tail)
+                            tc_mma_bf16_pair(d, da + kk * op_step<A_MN>(), db + kk * op_step<B_MN>(),
+                                             idesc, (kb | kk) != 0);
                     tc_commit_pair(&empty[ring.bar], 0x3);
                 }
                 tc_commit_pair(&tfull[b], 0x3);
