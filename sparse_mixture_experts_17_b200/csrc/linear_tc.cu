@@ -547,40 +547,19 @@ __device__ __forceinline__ TileAt tile_at(const PairArgs &p, const GroupSmem &G,
     return a;
 }
 
-// Calls f(tile, class) for a pair's tiles in order, until it returns false. Groups of
-// class 0 are bound by the tensor cores, the others by reading their weights. Where
-// a call has both, the even pairs begin with the one kind and the odd pairs with
-// the other, so that the two overlap and each pair changes its ring only twice.
+// Calls f(tile, ring class) for a pair's tiles in order, until it returns false. The groups
+// come by class, so a pair passes each ring once. (Starting half of the pairs with the
+// short groups, so that tiles bound by the tensor cores run beside tiles bound by
+// reading weights, changed nothing: 2482 us against 2447 for 256 skewed experts.)
 template <LinMode MODE, bool WIDE, class F>
 __device__ __forceinline__ void walk_tiles(const PairArgs &p, const GroupSmem &G, F f)
 {
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    if (MODE == LIN_DW) {
-        const int total = p.E * p.splits * p.m_tiles * p.c_tiles;
-        for (int t = pair; t < total; t += npairs)
-            if (!f(tile_at<MODE, WIDE>(p, G, t), 0))
-                return;
-        return;
-    }
-    const bool mixed = npairs > 1 && G.cls[1] > 0 && G.cls[1] < G.cls[3];
-    const bool odd = mixed && (pair & 1);
-#pragma unroll 1
-    for (int i = 0; i < 3; ++i) {
-        const int c = odd ? 2 - i : i;
-        int lo = G.cls[c] * p.m_tiles, hi = G.cls[c + 1] * p.m_tiles;
-        int at = pair, step = npairs;
-        if (mixed) {
-            const int even = (npairs + 1) / 2;
-            const int cut = lo + (int)((long long)(hi - lo) * even / npairs);
-            (odd ? lo : hi) = cut;
-            step = odd ? npairs / 2 : even;
-            at = pair >> 1;
-        }
-        if (c)   // the pairs that got one tile more of class 0 get one less here
-            at = step - 1 - at;
-        for (int t = lo + at; t < hi; t += step)
-            if (!f(tile_at<MODE, WIDE>(p, G, t), WIDE && c == 0 ? 3 : c))
-                return;
+    const int total = MODE == LIN_DW ? p.E * p.splits * p.m_tiles * p.c_tiles : G.cls[3] * p.m_tiles;
+    const int end0 = G.cls[1] * p.m_tiles, end1 = G.cls[2] * p.m_tiles;
+    for (int t = blockIdx.x >> 1; t < total; t += gridDim.x >> 1) {
+        const int c = MODE == LIN_DW ? 0 : t < end0 ? (WIDE ? 3 : 0) : t < end1 ? 1 : 2;
+        if (!f(tile_at<MODE, WIDE>(p, G, t), c))
+            return;
     }
 }
 
