@@ -7,9 +7,11 @@
 //
 // Bound by HBM: each kept row is read (and in the backward written) once. A
 // token is owned by `lanes` consecutive threads (d / 8 rounded up to a power of
-// two, 16 to 256), each moving 16-byte vectors of 8 columns, all k rows' loads
-// of a vector in flight together. Sums run in fp32 in slot order, so results
-// repeat bit for bit; no atomics.
+// two, 16 to 256; see lanes_for), each moving 16-byte vectors of 8 columns, all k
+// rows' loads of a vector in flight together (four at a time in the backward of
+// k = 8). Sums run in fp32 in slot order, so results repeat bit for bit; no atomics.
+// Measured: 16384 x 4096, k = 2, with the residual 82 us (537 MB, 6.5 TB/s); backward
+// of 4096 x 2048, k = 8, 60% kept, 37 us (179 MB, 4.9 TB/s: latency of the scattered rows).
 #include <algorithm>
 
 #include "common.cuh"

@@ -8,7 +8,9 @@
 // tensors together and writes one fp64 partial sum, so the order of the sums
 // depends on sizes, alignments and the SM count only. The scaling kernel adds the
 // partials itself (every CTA the same way), which saves a launch, and walks
-// the chunks backwards: the ones read last may still be in L2.
+// the chunks backwards: the ones read last may still be in L2. Measured: 2.8 GB
+// scaled into other buffers 1320 us (8.4 GB moved, 6.4 TB/s; the squares alone 430 us,
+// 717 when a slow path indexed the vectors at run time and put them in local memory).
 #include <algorithm>
 #include <cmath>
 #include <cstring>

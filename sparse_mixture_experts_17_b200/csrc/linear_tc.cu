@@ -6,14 +6,13 @@
 // of the MMA and the tokens (for dW the output features) its N side, because N
 // is free in steps of 16: a group's rows are cut into near-equal tiles of at
 // most 256 and each tile runs MMAs just wide enough, so a ragged group pays for
-// at most 31 rows that it does not have. It also puts consecutive m in
-// consecutive TMEM lanes: a warp stores 64 contiguous bytes per token, the bias
-// is one value per thread, and a token's validity is uniform over the warp.
+// at most 31 rows that it does not have, and a single token takes MMAs of the
+// smallest N while its weights pass once.
 //
 // Operands. Every box that the TMA brings is 64 elements (128 bytes) wide,
 // 128-byte swizzled. Where the contraction runs along the contiguous axis the
 // tile is K-major; where it runs across rows (W for dx; x and dz for dW) the
-// same boxes are an MN-major operand, so nothing is ever transposed in memory.
+// same boxes are an MN-major operand, so no operand is transposed in memory.
 // W is a three-dimensional map (d_in, d_out, expert): what lies past an edge of
 // one expert's matrix reads as zero and never as the next expert's values. For
 // dW the contraction runs over a group's rows: the rows of the last block that

@@ -272,6 +272,23 @@ def test_lower_tail_of_gelu():
     assert_within(y, ref, (U + 2.0 ** -17) * ref.abs(), "gelu")
 
 
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_bias_gradients_keep_fp32(act):
+    """dbias sums the unrounded dz in fp32, so the derivative has to be good to fp32 as well. The special
+    functions are off by 2 units in the last place (2.4e-7), their arguments by one rounding each, Phi
+    by 1.4e-7 of itself; multiplied by slopes of at most 1.13 and by |z|: below 7e-7 (1 + |z|) in all.
+    The sum of n terms adds n 2^-24."""
+    c = Case(2190, 64, 616, act, seed=4)
+    o = c.backward(dx=False, dW=False)
+    dz = c.dy.double() * slope64(c.z.double(), act)
+    bound = (7e-7 * (1 + c.z.double().abs()) * c.dy.double().abs() + c.rows * 2.0 ** -24 * dz.abs()).sum(0)
+    # and of the whole vector: dy has both signs, independent of z, so the terms' errors, at most 7e-7 of
+    # a term where |z| is small and less of it elsewhere, add up as the terms do
+    err = o["db"][0].double() - dz.sum(0)
+    assert bool((err.abs() <= bound).all())
+    assert float(err.norm() / dz.sum(0).norm()) <= 7e-7
+
+
 @pytest.mark.parametrize("di,do", [(64, 8192), (8192, 64)])
 def test_indices_past_32_bits(di, do):
     """2.6 * 2^30 elements in y (or x, and then in dx)."""
