@@ -300,16 +300,16 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][8],
 }
 
 // A warp's part of a tile: columns h * 16 + [0, 16), and every 16 NH from there, below
-// cn (NH warps share a lane quarter). Two chunks' loads go out together where the
-// registers allow it, and `release` runs as soon as the last value has left the
-// accumulator. res: of the first chunk; each next one's goes out a chunk ahead.
+// cn (NH warps share a lane quarter). res: the residual of the first chunk; each next
+// one's goes out a chunk ahead. `release` runs as soon as the last value has left the
+// accumulator.
 template <LinMode MODE, int ACT, int NH, class R>
 __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
                                            const float (&bias)[4], uint4 (&res)[kChunk / 8],
                                            long long c0, int m0, int M, int cn, int lane,
                                            const WarpStage &w, R release)
 {
-    constexpr int SKIP = kChunk * NH, STEP = MODE == LIN_FWD ? SKIP : 2 * SKIP;
+    constexpr int STEP = kChunk * NH;
     const int first = h * kChunk;
     if (m0 >= M || first >= cn) {
         release();
@@ -317,21 +317,15 @@ __device__ __forceinline__ void store_tile(const LinOut &o, uint32_t tb, int h,
     }
 #pragma unroll 1
     for (int c = first; c < cn; c += STEP) {
-        float v[2][8], v2[2][8];
+        float v[2][8];
         uint4 next[kChunk / 8];
         load_acc(tb + c, v);
-        const bool two = MODE != LIN_FWD && c + SKIP < cn;
-        if (two)
-            load_acc(tb + c + SKIP, v2);
         load_residual<MODE>(o, c0 + c + STEP, m0, M, min(kChunk, cn - c - STEP), lane, next);
         store_chunk<MODE, ACT>(o, v, bias, res, c0 + c, m0, M, min(kChunk, cn - c), lane, w, [&] {
             tmem_ld_wait();
             if (c + STEP >= cn)
                 release();
         });
-        if (two)
-            store_chunk<MODE, ACT>(o, v2, bias, res, c0 + c + SKIP, m0, M, min(kChunk, cn - c - SKIP),
-                                   lane, w, [] {});
 #pragma unroll
         for (int i = 0; i < kChunk / 8; ++i)
             res[i] = next[i];
