@@ -341,8 +341,8 @@ __device__ __forceinline__ void store_zeros(const LinOut &o, int warp, long long
         *reinterpret_cast<uint4 *>(o.out + (c0 + c) * o.ld + m) = make_uint4(0, 0, 0, 0);
 }
 
-// The same for fp32 partial sums of dW: a lane holds one m of 32 columns, and a
-// warp's store is 128 contiguous bytes.
+// fp32 partial sums of dW: a lane holds one m of 32 columns, and a warp's store is 128
+// contiguous bytes.
 __device__ __forceinline__ void store_part(float *part, long long ld, uint32_t taddr, bool zero,
                                            long long c0, int m, int M, int n)
 {
@@ -396,9 +396,9 @@ constexpr int kPairSmem = 1024 + kRingBytes + kPairBars + kEpiWarps * kStageByte
 // 64): the smaller the tokens' part of a stage, the more stages fit. A stage's round
 // trip (copy, MMAs, commit, the producer's wait) takes 1.9 us even on an idle GPU,
 // so 6 stages of 16 KB of weights let an SM read 51 GB/s, and 9 half as much again.
-// Each class has its own barriers; a CTA goes from one to another at most twice, and
-// only when every stage of the last one has been consumed.
-// Class 3 is for double tiles (up to 512 rows).
+// Each class has its own barriers; a CTA passes each class once, and goes to the next only
+// when every stage of the last one has been consumed. Class 3 is for double tiles (up to
+// 512 rows), in the place of class 0.
 __host__ __device__ constexpr int ring_stages(int c) { return c == 0 ? 6 : c == 1 ? 8 : c == 2 ? 9 : 4; }
 __host__ __device__ constexpr int ring_stage_bytes(int c)
 {
@@ -1323,11 +1323,11 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
     if (pair_tiles >= sms / 2 && avg > 32) {
         // Double tiles share the weights' part of a stage between 512 rows: a quarter less
         // from L2 for the same products, at the price of an epilogue that overlaps less.
-        // us single -> double: 16384 x 14336 -> 4096 1842 -> 1618, 4096 x 8192 -> 4096 in 8
-        // groups 307 -> 276, 16384 x 4096 -> 4096 554 -> 520, x 2048 297 -> 298, x 1024 170 ->
-        // 185; where the pairs' last round fills up worse (8192 x 2048 -> 4096 in 8) 154 -> 170.
+        // us single -> double: 16384 x 14336 -> 4096 1522 -> 1444, 4096 x 8192 -> 4096 in 8
+        // groups 263 -> 249, 16384 x 4096 -> 4096 469 -> 454, x 2048 256 -> 254, x 1024 149 ->
+        // 148; where the pairs' last round fills up worse (8192 x 2048 -> 4096 in 8) 132 -> 144.
         const long long pairs = sms / 2, half = (pair_tiles + 1) / 2;
-        if (avg >= 2 * kTileC && ceil_div(K, kBox) >= 64 &&
+        if (avg >= 2 * kTileC && ceil_div(K, kBox) >= 32 &&
             2 * ((half + pairs - 1) / pairs) <= (pair_tiles + pairs - 1) / pairs)
             return launch_pair<MODE, ACT, true>(a, st);
         return launch_pair<MODE, ACT>(a, st);
