@@ -229,6 +229,32 @@ def test_calls_in_a_row():
             assert torch.equal(o[k], o0[k]), (i, k)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, in flight together give what each gives alone."""
+    cases = [Case(900, 520, 2048, "gelu", offsets=sizes_to_offsets([600, 0, 250, 50]), seed=21),
+             Case(2100, 1024, 1032, "silu", seed=22)]
+    alone = [(c.forward()[0], c.backward()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [M.alloc_linear_workspace(c.shape) for c in cases]
+    got = [[(torch.full((c.rows, c.do), 7.0, dtype=BF16, device="cuda"),
+             dict(dx=torch.full_like(c.x, 5.0), dW=torch.empty_like(c.W), db=torch.empty_like(c.bias)))
+            for _ in range(8)] for c in cases]
+    torch.cuda.synchronize()
+    for n in range(8):
+        for c, st, w, out in zip(cases, streams, ws, got):
+            y, o = out[n]
+            M.moe_linear_forward(c.shape, c.x, c.offsets, c.W, c.bias, c.R, y, None, c.status, stream=st)
+            M.moe_linear_backward(c.shape, c.x, c.offsets, c.W, c.z, c.dy, o["dx"], o["dW"], o["db"], c.status, w,
+                                  stream=st)
+    torch.cuda.synchronize()
+    for (y0, o0), out, c in zip(alone, got, cases):
+        assert int(c.status.item()) == 0
+        for y, o in out:
+            assert torch.equal(y, y0)
+            for k in o:
+                assert torch.equal(o[k], o0[k]), k
+
+
 def test_dx_feeds_the_next_call_at_once():
     """A chain of products, each backward fed by the one before without a wait, equals the same with
     waits: the last kernel of a call ends after all others of it."""
