@@ -72,9 +72,11 @@ __device__ __forceinline__ float act_grad_f(float z)
     if (ACT == MOE_ACT_GELU)   // Phi(z) + z phi(z)
         return fmaf(0.39894228040143268f * z, exp2_fast(-0.72134752f * z * z), normal_cdf(z));
     if (ACT == MOE_ACT_GELU_TANH) {
-        // d/dz [z s(v)] = s + z s (1 - s) v', v = 2u, v' = 2 sqrt(2/pi)(1 + 3 0.044715 z^2)
+        // d/dz [z s(v)] = s + z s (1 - s) v', v = 2u, v' = 2 sqrt(2/pi)(1 + 3 0.044715 z^2).
+        // From |z| = 11 on s (1 - s) is 0 in fp32; the last factor, which leaves fp32 at 5e19,
+        // is kept finite so that the product is 0 as well (a NaN comes through s).
         const float s = sigmoid_f(gelu_tanh_2u(z));
-        return s + z * s * (1.f - s) * 1.5957691216057308f * fmaf(0.134145f * z, z, 1.f);
+        return s + z * s * (1.f - s) * 1.5957691216057308f * fminf(fmaf(0.134145f * z, z, 1.f), 3e38f);
     }
     if (ACT == MOE_ACT_SILU) {
         const float s = sigmoid_f(z);
