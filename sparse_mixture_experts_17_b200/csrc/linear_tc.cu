@@ -284,10 +284,15 @@ __device__ __forceinline__ void store_chunk(const LinOut &o, float (&v)[2][8],
         uint32_t r[4];
         if (MODE == LIN_FWD && o.residual)
             ldmatrix4_t(w.mat + ci * 512, r);
+        float f[2][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i >> 2][i & 3] = v[i >> 2][4 * ci + (i & 3)];
+        act_n<ACT>(f[0]);
+        act_n<ACT>(f[1]);
 #pragma unroll
         for (int mi = 0; mi < 4; ++mi) {
-            const int k = 4 * ci + 2 * (mi & 1);
-            float a = act_f<ACT>(v[mi >> 1][k]), b = act_f<ACT>(v[mi >> 1][k + 1]);
+            float a = f[mi >> 1][2 * (mi & 1)], b = f[mi >> 1][2 * (mi & 1) + 1];
             if (MODE == LIN_FWD && o.residual) {
                 a += bf16lo(r[mi]);
                 b += bf16hi(r[mi]);
@@ -1075,8 +1080,9 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
                     if (p.o.z)
                         *reinterpret_cast<uint2 *>(p.o.z + at) =
                             make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-                    sum.x = act_f<ACT>(sum.x), sum.y = act_f<ACT>(sum.y);
-                    sum.z = act_f<ACT>(sum.z), sum.w = act_f<ACT>(sum.w);
+                    float v[4] = {sum.x, sum.y, sum.z, sum.w};
+                    act_n<ACT>(v);
+                    sum = make_float4(v[0], v[1], v[2], v[3]);
                     if (p.o.residual) {
                         sum.x += bf16lo(res.x), sum.y += bf16hi(res.x);
                         sum.z += bf16lo(res.y), sum.w += bf16hi(res.y);

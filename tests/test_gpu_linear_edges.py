@@ -1,5 +1,7 @@
 """The linear products' activations far from zero: the derivative of gelu's tanh form where
-z^2 leaves fp32."""
+z^2 leaves fp32, and the lower tail of gelu."""
+import math
+
 import pytest
 import torch
 
@@ -43,3 +45,30 @@ def test_derivatives_of_huge_values(act):
     assert bool(torch.isfinite(ref).all())
     assert_within(db, ref, torch.full_like(ref, 2.0 ** -18), "derivative")
     assert_within(dx[0], ref, U * ref.abs() + 2.0 ** -17, "dz")
+
+
+def test_tail_of_gelu_past_six():
+    """gelu(z) and its derivative for z from -12.9 to -6 keep their relative accuracy: Phi to 2^-10 (its
+    logarithm is a cubic there, 6.5e-4 off at most), and one rounding to bf16. Below, where Phi is
+    under fp32's smallest normal number, it counts as 0."""
+    z = torch.linspace(-12.9, -6, 1024, device="cuda").to(BF16)
+    n = z.numel()
+    W = torch.zeros(n, 8, dtype=BF16, device="cuda")
+    W[:, 0] = z
+    x = torch.zeros(3, 8, dtype=BF16, device="cuda")
+    x[:, 0] = 1.0
+    y = torch.empty(3, n, dtype=BF16, device="cuda")
+    M.moe_linear_forward(M.make_linear(3, 8, n, act=M.MOE_ACT_GELU), x, None, W, None, None, y)
+    z64 = z.double()
+    Phi = 0.5 * torch.special.erfc(-z64 * math.sqrt(0.5))      # torch's ndtr is (1 + erf) / 2: 1e-16 off here
+    ref = (z64 * Phi).expand(3, -1)
+    assert_within(y, ref, (U + 2.0 ** -10) * ref.abs(), "gelu")
+    db, _ = slopes(z, "gelu")
+    ref = Phi + z64 * torch.exp(-0.5 * z64 * z64) / math.sqrt(2 * math.pi)
+    assert_within(db, ref, 2.0 ** -10 * ref.abs(), "derivative of gelu")
+    far = torch.tensor([-13.5, -14.0, -20.0, -100.0, -1e19, -1e30, -3e38, -3.38e38], device="cuda").to(BF16)
+    W = torch.zeros(8, 8, dtype=BF16, device="cuda")
+    W[:, 0] = far
+    y = torch.empty(3, 8, dtype=BF16, device="cuda")
+    M.moe_linear_forward(M.make_linear(3, 8, 8, act=M.MOE_ACT_GELU), x, None, W, None, None, y)
+    assert bool((y.abs().double() <= 2.0 ** -122).all())
