@@ -561,8 +561,8 @@ MOE_API int moe_linear_forward(const moe_linear_t *shape, const moe_bf16_t *x,
  *   dW [E, d_out, d_in] bf16 out or NULL; dbias [E, d_out] fp32 out or NULL:
  *      fully written (zero for an empty group, and for rows = 0)
  * Outputs overlap no input. W may be NULL when dx is, x when dW is. With an
- * activation dz is rounded to bf16 for the products (dbias sums it
- * unrounded). The same inputs give the same bits on every call. Calls that
+ * activation dz is rounded to bf16 for the products; dbias sums it
+ * unrounded, in fp32 over at most 32 rows and in fp64 beyond. The same inputs give the same bits on every call. Calls that
  * share a workspace must be ordered on the GPU, replays of captured graphs
  * among them. Device errors: MOE_ERR_CHECK (offsets), MOE_ERR_TIMEOUT. */
 MOE_API int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,

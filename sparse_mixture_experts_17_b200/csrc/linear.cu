@@ -107,30 +107,32 @@ __global__ void __launch_bounds__(256, kDzCtasPerSm)
 }
 
 // db[e] = sum of the group's items (0 for an empty group). A CTA of 32 columns x 8:
-// each of the 8 adds every eighth item, and their sums are added in order.
+// each of the 8 adds every eighth item, and their sums are added in order. In fp64: an item
+// is 10 fp32 additions deep, but a group of 2^24 rows has 65,536 items for each of the 8,
+// and terms of one sign and size left such a chain 5.5e-4 off in fp32 (2.4e-5 at 2^19 rows).
 __global__ void __launch_bounds__(256)
     k_linear_db(const float *__restrict__ part, float *db, const int32_t *offsets, int E, int rows,
                 int d_out)
 {
     __shared__ GroupSmem G;
-    __shared__ float red[8][32];
+    __shared__ double red[8][32];
     pdl_wait();
     pdl_trigger();
     build_groups(G, offsets, E, rows, kDzRows, nullptr);
     const int e = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float s = 0.f;
+    double s = 0.0;
     if (c < d_out)
 #pragma unroll 4
         for (int i = G.first[e] + w; i < G.first[e + 1]; i += 8)
-            s += part[(long long)i * d_out + c];
+            s += (double)part[(long long)i * d_out + c];
     red[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < d_out) {
 #pragma unroll
         for (int k = 1; k < 8; ++k)
             s += red[k][lane];
-        db[(long long)e * d_out + c] = s;
+        db[(long long)e * d_out + c] = (float)s;
     }
 }
 

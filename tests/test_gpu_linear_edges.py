@@ -1,12 +1,12 @@
-"""The linear products' activations far from zero: the derivative of gelu's tanh form where
-z^2 leaves fp32, and the lower tail of gelu."""
+"""The linear products' activations far from zero (the derivative of gelu's tanh form where z^2
+leaves fp32, the lower tail of gelu), and the bias gradients of long groups."""
 import math
 
 import pytest
 import torch
 
 from sparse_mixture_experts_17_b200 import moe as M
-from test_gpu_linear import ACTS, BF16, F32, U, assert_within, slope64
+from test_gpu_linear import ACTS, BF16, F32, U, assert_within, sizes_to_offsets, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,24 @@ def test_tail_of_gelu_past_six():
     y = torch.empty(3, 8, dtype=BF16, device="cuda")
     M.moe_linear_forward(M.make_linear(3, 8, 8, act=M.MOE_ACT_GELU), x, None, W, None, None, y)
     assert bool((y.abs().double() <= 2.0 ** -122).all())
+
+
+@pytest.mark.parametrize("sizes", [[1 << 20], [1 << 19, 0, 33, 1 << 20]])
+def test_bias_gradients_of_long_groups(sizes):
+    """The bias gradient of a group of a million rows, with terms of one sign and one value (what the mean of
+    a loss gives), keeps fp32's bits: at most 12 fp32 additions in a row, and fp64 from there. dz carries
+    the derivative's 7e-7 (1 + |z|) = 1.4e-6 of dy, the product's rounding and the sums' 13."""
+    off = sizes_to_offsets(sizes)
+    rows, E = off[-1], len(sizes)
+    z = torch.ones(rows, 8, dtype=BF16, device="cuda")
+    dy = torch.full((rows, 8), 0.1, dtype=BF16, device="cuda")
+    db = torch.empty(E, 8, dtype=F32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = M.make_linear(rows, 8, 8, E=E, act=M.MOE_ACT_SILU)
+    M.moe_linear_backward(s, None, torch.tensor(off, dtype=torch.int32, device="cuda"), None, z, dy, None, None, db,
+                          status, M.alloc_linear_workspace(s))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    slope = float(slope64(torch.ones(1, dtype=torch.float64), "silu"))
+    ref = torch.tensor(sizes, dtype=torch.float64, device="cuda")[:, None] * float(dy[0, 0]) * slope
+    assert_within(db, ref.expand(E, 8), (1.4e-6 / slope + 14 * 2.0 ** -24) * ref, "db")
