@@ -573,8 +573,8 @@ MOE_API int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
 
 /* ---- Combine of bf16 expert rows and its gradient ("Sparse MoE Block": scale by
  * the routing weight, index_add into token order), for expert rows that
- * moe_linear_forward wrote. Only T, d and k of the shape are used (its rules
- * apply to all fields).
+ * moe_linear_forward wrote. Of the shape only T, d, E and k count, by their rules but
+ * for d, which is any multiple of 8 in [8, 65536]; the other fields may hold anything.
  * moe_combine_rows:
  *   out[t] = residual[t] + sum_{j, slot_pos[t,j] >= 0} w[t,j] y_perm[slot_pos[t,j]]
  *   y_perm [T*k, d] bf16; slot_pos [T, k] int32 (moe_permute; negative: dropped);
@@ -587,6 +587,7 @@ MOE_API int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
  *   dtopk_w[t,j] = <dout[t], y_perm[slot_pos[t,j]]>, 0 for a dropped slot
  *   y_perm may be NULL when dtopk_w is; dy_perm or dtopk_w may be NULL. Each row
  *   of dy_perm is the slot of at most one (t, j).
+ * Outputs overlap no input and no other output, but for out and residual.
  * A slot_pos >= T*k is treated as dropped and sets MOE_ERR_CHECK in *status. */
 MOE_API int moe_combine_rows(const moe_shape_t *shape, const moe_bf16_t *y_perm,
                              const int32_t *slot_pos, const float *topk_w,

@@ -204,6 +204,16 @@ int lanes_for(int nv, int T)
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Rows of any width that a linear product writes: the fields that the combine does not use
+// may hold anything, d is its own rule.
+int check_rows_shape(const moe_shape_t *s)
+{
+    if (!s || s->T < 0 || s->T > (1 << 24) || s->E < 1 || s->E > MOE_MAX_E || s->k < 1 ||
+        s->k > std::min(s->E, MOE_MAX_K) || s->d < 8 || s->d > 65536 || s->d % 8 != 0)
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 template <int K>
 int launch_fwd(const moe_shape_t &s, const uint16_t *y, const int32_t *slot, const float *w,
                const uint16_t *res, uint16_t *out, uint32_t *status, cudaStream_t st)
@@ -237,7 +247,7 @@ int moe_combine_rows(const moe_shape_t *shape, const moe_bf16_t *y_perm, const i
                      const float *topk_w, const moe_bf16_t *residual, moe_bf16_t *out,
                      uint32_t *status, moe_stream_t stream)
 {
-    int rc = check_shape(shape);
+    const int rc = check_rows_shape(shape);
     if (rc)
         return rc;
     if (shape->T == 0)
@@ -264,7 +274,7 @@ int moe_combine_rows_backward(const moe_shape_t *shape, const moe_bf16_t *dout,
                               const float *topk_w, moe_bf16_t *dy_perm, float *dtopk_w,
                               uint32_t *status, moe_stream_t stream)
 {
-    int rc = check_shape(shape);
+    const int rc = check_rows_shape(shape);
     if (rc)
         return rc;
     if (shape->T == 0)

@@ -492,7 +492,8 @@ _COMBINE_ROWS = (("y_perm", "slot_pos", "topk_w", "residual", "out", "status"),
 
 
 def moe_combine_rows(shape, y_perm, slot_pos, topk_w, residual, out, status=None, stream=None):
-    """out[t] = residual[t] + sum_j w[t,j] y_perm[slot_pos[t,j]], bf16 rows (topk_w None: all 1)."""
+    """out[t] = residual[t] + sum_j w[t,j] y_perm[slot_pos[t,j]], bf16 rows (topk_w None: all 1).
+    The shape's T, d, E and k count; d is any multiple of 8."""
     T, d, k = shape.T, shape.d, shape.k
     ptrs, on_device = _args(*_COMBINE_ROWS, ((T * k, d), (T, k), (T, k), (T, d), (T, d), 1),
                             (y_perm, slot_pos, topk_w, residual, out, status))
