@@ -96,13 +96,15 @@ enum {
                                         MOE_ERR_CHECK; the workspace holds one int32 per
                                         assignment more. A build with -DMOE_DEBUG sets it on
                                         every call */,
-    MOE_FLAG_TEST_TIMEOUT = 1 << 13  /* test only, honoured by moe_expert_ffn alone: its w1/w3
-                                        GEMM runs on the single-SM tensor-core kernel with a
-                                        producer that issues no loads and pipeline waits
-                                        bounded at 50 ms, so every CTA gives up its first wait,
-                                        flags MOE_ERR_TIMEOUT, frees its tensor memory and
-                                        returns with nothing in flight. Exercises the bounded
-                                        waits; the call's results are meaningless */
+    MOE_FLAG_TEST_TIMEOUT = 1 << 13  /* test only: pipeline waits are bounded at 50 ms and a
+                                        producer stops, so that the kernels give up, flag
+                                        MOE_ERR_TIMEOUT, free their tensor memory and return;
+                                        the call's results are meaningless. Honoured by
+                                        moe_expert_ffn (its w1/w3 GEMM on the single-SM
+                                        tensor-core kernel; nothing is loaded) and, as
+                                        moe_linear_t.flags, by moe_linear_forward and
+                                        moe_linear_backward (one CTA of each cluster stops
+                                        before the last block of its contraction) */
 };
 
 #define MOE_MAX_E 256
@@ -522,7 +524,7 @@ enum {
 
 /* Shape of a linear product. Requirements (else MOE_ERR_INVALID_ARG):
  *   0 <= rows <= 2^24; d_in and d_out multiples of 8 in [8, 65536];
- *   1 <= E <= MOE_MAX_E; act one of MOE_ACT_*; flags 0.
+ *   1 <= E <= MOE_MAX_E; act one of MOE_ACT_*; flags 0 (or MOE_FLAG_TEST_TIMEOUT).
  * Groups: expert_offsets [E+1] int32 on the device (as moe_permute writes
  * them), 0 <= offsets[0] <= ... <= offsets[E] <= rows; groups may be empty,
  * and rows outside every group are neither read into a result nor written.

@@ -109,8 +109,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// Wall-clock bound of one wait: far above any legitimate pipeline stall.
+// Wall-clock bound of one wait: far above any legitimate pipeline stall; and the bound
+// of the launches that MOE_FLAG_TEST_TIMEOUT starves.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kTestWaitLimitNs = 50000000ull;
 
 // Wait for the phase of `bar` with the given parity to complete. Returns false
 // (after flagging MOE_ERR_TIMEOUT and raising *abort) if it does not complete
@@ -309,7 +311,8 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
 // Bounded wait with cluster-scope acquire (for barriers that receive arrivals
 // from the peer CTA); same limits and abort protocol as mbar_wait.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity,
-                                                  volatile int *abort, uint32_t *status)
+                                                  volatile int *abort, uint32_t *status,
+                                                  uint64_t limit_ns = kWaitLimitNs)
 {
 #pragma unroll 1
     for (int i = 0; i < 128; ++i)
@@ -322,7 +325,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
             return true;
         if (*abort)
             return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (globaltimer_ns() - t0 > limit_ns) {
             *abort = 1;
             flag_status(status, MOE_ERR_TIMEOUT);
             return false;

@@ -882,9 +882,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 
 // ---------------------------------------------------------------- host side
 
-// Wait bound of the test-only starved launch (GemmArgs::test_starve).
-constexpr unsigned long long kTestWaitLimitNs = 50000000ull;
-
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

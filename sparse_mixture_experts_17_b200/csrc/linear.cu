@@ -144,7 +144,8 @@ int check_linear(const moe_linear_t *s)
         return MOE_ERR_INVALID_ARG;
     auto dim = [](int v) { return v >= 8 && v <= 65536 && v % 8 == 0; };
     if (s->rows < 0 || s->rows > (1 << 24) || s->E < 1 || s->E > MOE_MAX_E || !dim(s->d_in) ||
-        !dim(s->d_out) || s->act < MOE_ACT_NONE || s->act > MOE_ACT_SILU || s->flags != 0)
+        !dim(s->d_out) || s->act < MOE_ACT_NONE || s->act > MOE_ACT_SILU ||
+        (s->flags & ~MOE_FLAG_TEST_TIMEOUT) != 0)
         return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
@@ -254,6 +255,7 @@ int moe_linear_forward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.d_out = s.d_out;
     p.E = s.E;
     p.act = s.act;
+    p.starve = (s.flags & MOE_FLAG_TEST_TIMEOUT) != 0;
     p.status = status;
     return launch_linear(LIN_FWD, p, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -310,6 +312,7 @@ int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.d_in = s.d_in;
     p.d_out = s.d_out;
     p.E = s.E;
+    p.starve = (s.flags & MOE_FLAG_TEST_TIMEOUT) != 0;
     p.status = status;
     // dz (if any) has completed when the bias sums start, and those when dx starts, ...:
     // each of the three lets its successor start only after its own wait, and none

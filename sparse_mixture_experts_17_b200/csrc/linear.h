@@ -30,6 +30,7 @@ struct LinArgs {
     // beside that kernel's last CTAs, and waits for it only before it ends (so that
     // whatever waits for this product has waited for both).
     bool late;
+    bool starve;                  // MOE_FLAG_TEST_TIMEOUT
     uint32_t *status;
 };
 

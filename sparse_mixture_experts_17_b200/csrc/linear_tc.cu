@@ -471,6 +471,10 @@ struct PairArgs {
     Divisor by_m, by_c, by_split;   // m_tiles, c_tiles, splits
     bool a_wide, b_wide;   // MN-major operands: two boxes in one copy
     bool late;       // see LinArgs
+    // Bound of every wait. starve (test only): the second CTA's producer stops before the last
+    // K block of its first tile, so that block's stage never fills on either side.
+    unsigned long long wait_ns;
+    bool starve;
     LinOut o;
     uint32_t *status;
 };
@@ -619,6 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (lane == 0) {   // ---------------- producer (both CTAs)
             Ring ring(WIDE ? 3 : 0);
             const uint32_t smem0 = smem_u32(smem), full0 = mapa_shared(smem_u32(full), 0);
+            const int skip = p.starve && !leader ? 1 : 0;
             walk_tiles<MODE, WIDE>(p, G, [&](const TileAt &a, int c) {
                 const int half = ((a.cn + 31) & ~31) / 2;      // c of this CTA
                 const int c0 = a.c0 + (int)rank * half, m0 = a.m0 + 128 * (int)rank;
@@ -632,12 +637,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     kPairABytes + (MODE == LIN_DW ? (p.b_wide ? 2 : nb) * kBoxBytes : 2048 << fit) +
                     (half2 ? 2048 << fit2 : 0);
                 if (MODE != LIN_DW && c != ring.cls) {   // another ring over the same memory
-                    if (ring.used && !mbar_wait(&empty[ring.last()], ring.last_phase(), abort_flag, p.status))
+                    if (ring.used && !mbar_wait(&empty[ring.last()], ring.last_phase(), abort_flag,
+                                                p.status, p.wait_ns))
                         return false;
                     ring = Ring(c);
                 }
-                for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!mbar_wait(&empty[ring.bar], ring.phase ^ 1u, abort_flag, p.status))
+                for (int kb = 0; kb < a.nkb - skip; ++kb) {
+                    if (!mbar_wait(&empty[ring.bar], ring.phase ^ 1u, abort_flag, p.status, p.wait_ns))
                         return false;
                     const uint32_t sa = smem0 + ring.at, sb = sa + kPairABytes;
                     const bool tail = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
@@ -674,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             tma_4d_pair(sb + j * kBoxBytes, tb, c0 + j * kBox, ka, 0, 0, bar);
                     }
                 }
-                return true;
+                return skip == 0;
             });
         }
     } else if (warp == 1) {
@@ -694,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                          add || kk != 0);
             };
             const auto wait_full = [&](const Ring &r) {
-                const bool ok = mbar_wait(&full[r.bar], r.phase, abort_flag, p.status);
+                const bool ok = mbar_wait(&full[r.bar], r.phase, abort_flag, p.status, p.wait_ns);
                 tc_fence_after();
                 return ok;
             };
@@ -706,7 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t b = local & 1u, aph = (local >> 1) & 1u;
                 ++local;
                 const uint32_t idesc = lin_idesc<MODE>(256, (a.cn + 31) & ~31);
-                if (!mbar_wait(&tempty[b], aph ^ 1u, abort_flag, p.status))
+                if (!mbar_wait(&tempty[b], aph ^ 1u, abort_flag, p.status, p.wait_ns))
                     return false;
                 tc_fence_after();
                 const uint32_t d = tmem_base + b * kTileC;
@@ -726,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             return false;
                         mma(d, idesc, r, kPairABytes, kb != 0, kBox);
                     }
-                    if (!mbar_wait(&tempty[b2], aph2 ^ 1u, abort_flag, p.status))
+                    if (!mbar_wait(&tempty[b2], aph2 ^ 1u, abort_flag, p.status, p.wait_ns))
                         return false;
                     tc_fence_after();
                     for (int kb = 0; kb < head; ++kb, ring.next()) {
@@ -759,9 +765,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     // stalls the issue for longer than a stage's MMAs take, so only
                     // a last block, whose zeros the peer wrote, waits with it.
                     const bool last = MODE == LIN_DW && a.tail && kb == a.nkb - 1;
-                    if (last && !mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status))
+                    if (last && !mbar_wait_cluster(&full[ring.bar], ring.phase, abort_flag, p.status,
+                                                   p.wait_ns))
                         return false;
-                    if (!mbar_wait(&full[ring.bar], ring.phase, abort_flag, p.status))
+                    if (!mbar_wait(&full[ring.bar], ring.phase, abort_flag, p.status, p.wait_ns))
                         return false;
                     tc_fence_after();
                     const uint64_t da = op_desc<A_MN>(smem0 + ring.at, 0);
@@ -784,7 +791,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (!a.tail)
                 return true;
             const uint32_t s = (it - 1) % ring_stages(0);
-            if (!__all_sync(kFullMask, mbar_wait(&tailbar[s], (phases >> s) & 1u, abort_flag, p.status)))
+            if (!__all_sync(kFullMask, mbar_wait(&tailbar[s], (phases >> s) & 1u, abort_flag, p.status,
+                                                 p.wait_ns)))
                 return false;
             phases ^= 1u << s;
             // row r of a 64 x 64 box is its bytes [128 r, 128 r + 128): the swizzle
@@ -822,7 +830,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 uint4 res[kChunk / 8];
                 load_residual<MODE>(p.o, c0 + h * kChunk, m0, M, min(kChunk, cn - h * kChunk), lane, res);
                 if (!none) {
-                    if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status)))
+                    if (!__all_sync(kFullMask, mbar_wait(&tfull[b], aph, abort_flag, p.status,
+                                                         p.wait_ns)))
                         return false;
                     ++local;
                     tc_fence_after();
@@ -856,6 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull)
             ;
+        __syncwarp();
     }
     tc_fence_before();
     cluster_sync_all();   // neither CTA leaves while the pair's MMAs may read its memory
@@ -891,6 +901,10 @@ struct SplitArgs {
     int kblocks;
     bool a_wide;
     bool late;       // see LinArgs
+    // Bound of every wait. starve (test only): the producer of each cluster's last CTA stops
+    // before its last K block.
+    unsigned long long wait_ns;
+    bool starve;
     LinOut o;
     uint32_t *status;
 };
@@ -963,9 +977,10 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
     if (warp == 0 && lane == 0) {   // ---------------- producer
         const int nb = (cn + C::BOXROWS - 1) / C::BOXROWS;
         const uint32_t bytes = C::A_BYTES + nb * C::BOXROWS * 128;
-        for (int i = 0; i < nkb; ++i) {
+        const int loads = p.starve && rank == p.S - 1 ? nkb - 1 : nkb;
+        for (int i = 0; i < loads; ++i) {
             const int s = i % C::STAGES;
-            if (!mbar_wait(&empty[s], ((i / C::STAGES) & 1u) ^ 1u, abort_flag, p.status))
+            if (!mbar_wait(&empty[s], ((i / C::STAGES) & 1u) ^ 1u, abort_flag, p.status, p.wait_ns))
                 break;
             uint8_t *sa = smem + s * C::STAGE, *sb = sa + C::A_BYTES;
             mbar_arrive_expect_tx(&full[s], bytes);
@@ -986,7 +1001,7 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int s = i % C::STAGES;
-            if (!mbar_wait(&full[s], (i / C::STAGES) & 1u, abort_flag, p.status)) {
+            if (!mbar_wait(&full[s], (i / C::STAGES) & 1u, abort_flag, p.status, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -1013,7 +1028,7 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         load_bias<MODE>(p.o, (long long)e * p.d_out, mq, M, lane, bias);
         load_residual<MODE>(p.o, c0 + h * kChunk, mq, M, min(kChunk, cn - h * kChunk), lane, res);
     }
-    const bool got = __all_sync(kFullMask, mbar_wait(done, 0, abort_flag, p.status));
+    const bool got = __all_sync(kFullMask, mbar_wait(done, 0, abort_flag, p.status, p.wait_ns));
     tc_fence_after();
     if (p.S == 1) {
         // the ring, which every copy and MMA has left, holds the rows on their way out
@@ -1098,6 +1113,7 @@ __global__ void __launch_bounds__(256, BC <= 128 ? 2 : 1)
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull)
             ;
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -1252,6 +1268,8 @@ int launch_pair(const LinArgs &a, cudaStream_t st)
     p.b_wide = b_wide;
     p.late = a.late;
     p.o = out_of(MODE, a);
+    p.wait_ns = a.starve ? kTestWaitLimitNs : kWaitLimitNs;
+    p.starve = a.starve;
     p.status = a.status;
     const long long tiles =
         MODE == LIN_DW ? (long long)a.E * p.splits * p.m_tiles * p.c_tiles
@@ -1295,6 +1313,8 @@ int launch_split(const LinArgs &a, int S, cudaStream_t st)
     p.late = a.late;
     p.kblocks = ceil_div(MODE == LIN_FWD ? a.d_in : a.d_out, kBox);
     p.o = out_of(MODE, a);
+    p.wait_ns = a.starve ? kTestWaitLimitNs : kWaitLimitNs;
+    p.starve = a.starve;
     p.status = a.status;
     const int m_tiles = ceil_div(MODE == LIN_FWD ? a.d_out : a.d_in, 128);
     // a group of n rows has at most n / BC + 1 items, and none when it is empty
