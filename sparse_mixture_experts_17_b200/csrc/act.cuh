@@ -62,19 +62,12 @@ __device__ __forceinline__ float normal_cdf_of(float z, float q)
     return z > 0.f ? 1.f - h : h;
 }
 
-__device__ __forceinline__ float normal_cdf(float z)
-{
-    const float m = fabsf(z), a = fminf(m, 6.f);
-    return normal_cdf_of(z, normal_q_tail(m - a, normal_q(a)));
-}
-
+// Every activation but gelu, which goes by normal_cdf_n.
 template <int ACT>
 __device__ __forceinline__ float act_f(float z)
 {
     if (ACT == MOE_ACT_RELU)
         return z > 0.f || z != z ? z : 0.f;   // NaN stays
-    if (ACT == MOE_ACT_GELU)
-        return z * normal_cdf(z);
     if (ACT == MOE_ACT_GELU_TANH)
         return z * sigmoid_f(gelu_tanh_2u(z));
     if (ACT == MOE_ACT_SILU)
@@ -82,32 +75,39 @@ __device__ __forceinline__ float act_f(float z)
     return z;
 }
 
-// act of N values in place. gelu's values past 6 are rare, so the tail is passed by where
-// none of the N is there (the same bits either way). 16384 x 256 -> 4096, us: 83 with N = 4
-// or 8, 86 with 2, 87 with the tail's four operations for every value, 79 without a tail.
-template <int ACT, int N>
-__device__ __forceinline__ void act_n(float (&v)[N])
+// Phi of N values. Values past 6 are rare, so the tail is passed by where none of the N is
+// there (the same bits either way). y = gelu(16384 x 256 -> 4096), us: 83 with N = 4 or 8, 86
+// with 2, 87 with the tail's four operations for every value, 79 without a tail; dz of 4096 x
+// 4096 with the bias sums: 24.7 with N = 4, 25.1 with 2 or 8 (which spills), 23.5 without.
+template <int N>
+__device__ __forceinline__ void normal_cdf_n(const float (&z)[N], float (&phi)[N])
 {
-    if (ACT == MOE_ACT_GELU) {
-        float q[N], top = 0.f;
+    float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            top = fmaxf(top, fabsf(v[i]));
-            q[i] = normal_q(fminf(fabsf(v[i]), 6.f));
-        }
-        if (top > 6.f) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                q[i] = normal_q_tail(fabsf(v[i]) - fminf(fabsf(v[i]), 6.f), q[i]);
-        }
+    for (int i = 0; i < N; ++i) {
+        top = fmaxf(top, fabsf(z[i]));
+        phi[i] = normal_q(fminf(fabsf(z[i]), 6.f));
+    }
+    if (top > 6.f) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] *= normal_cdf_of(v[i], q[i]);
-        return;
+            phi[i] = normal_q_tail(fabsf(z[i]) - fminf(fabsf(z[i]), 6.f), phi[i]);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        v[i] = act_f<ACT>(v[i]);
+        phi[i] = normal_cdf_of(z[i], phi[i]);
+}
+
+// act of N values in place.
+template <int ACT, int N>
+__device__ __forceinline__ void act_n(float (&v)[N])
+{
+    float phi[N];
+    if (ACT == MOE_ACT_GELU)
+        normal_cdf_n(v, phi);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = ACT == MOE_ACT_GELU ? v[i] * phi[i] : act_f<ACT>(v[i]);
 }
 
 template <int ACT>
@@ -115,8 +115,6 @@ __device__ __forceinline__ float act_grad_f(float z)
 {
     if (ACT == MOE_ACT_RELU)
         return z > 0.f ? 1.f : 0.f;
-    if (ACT == MOE_ACT_GELU)   // Phi(z) + z phi(z)
-        return fmaf(0.39894228040143268f * z, exp2_fast(-0.72134752f * z * z), normal_cdf(z));
     if (ACT == MOE_ACT_GELU_TANH) {
         // d/dz [z s(v)] = s + z s (1 - s) v', v = 2u, v' = 2 sqrt(2/pi)(1 + 3 0.044715 z^2).
         // From |z| = 11 on s (1 - s) is 0 in fp32; the last factor, which leaves fp32 at 5e19,
@@ -129,6 +127,20 @@ __device__ __forceinline__ float act_grad_f(float z)
         return s * (1.f + z * (1.f - s));
     }
     return 1.f;
+}
+
+// act' of N values in place.
+template <int ACT, int N>
+__device__ __forceinline__ void act_grad_n(float (&v)[N])
+{
+    float phi[N];
+    if (ACT == MOE_ACT_GELU)   // Phi(z) + z phi(z)
+        normal_cdf_n(v, phi);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = ACT == MOE_ACT_GELU
+                   ? fmaf(0.39894228040143268f * v[i], exp2_fast(-0.72134752f * v[i] * v[i]), phi[i])
+                   : act_grad_f<ACT>(v[i]);
 }
 
 } // namespace moe

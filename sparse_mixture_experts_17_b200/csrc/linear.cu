@@ -70,12 +70,21 @@ __global__ void __launch_bounds__(256, kDzCtasPerSm)
                         const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
                         const uint32_t zw[4] = {zz[u].x, zz[u].y, zz[u].z, zz[u].w};
                         uint32_t ow[4];
+                        float slope[2][4];
+                        if (ACT != MOE_ACT_NONE) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                slope[q][0] = bf16lo(zw[2 * q]), slope[q][1] = bf16hi(zw[2 * q]);
+                                slope[q][2] = bf16lo(zw[2 * q + 1]), slope[q][3] = bf16hi(zw[2 * q + 1]);
+                                act_grad_n<ACT>(slope[q]);
+                            }
+                        }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float a = bf16lo(gw[q]), b = bf16hi(gw[q]);
                             if (ACT != MOE_ACT_NONE) {
-                                a *= act_grad_f<ACT>(bf16lo(zw[q]));
-                                b *= act_grad_f<ACT>(bf16hi(zw[q]));
+                                a *= slope[q >> 1][2 * (q & 1)];
+                                b *= slope[q >> 1][2 * (q & 1) + 1];
                             }
                             sum[2 * q] += a;
                             sum[2 * q + 1] += b;
