@@ -60,11 +60,13 @@ enum {
     MOE_ERR_UNSUPPORTED = 2, /* valid request that the library does not implement */
     MOE_ERR_WORKSPACE = 3,   /* ws too small or misaligned */
     MOE_ERR_CUDA = 4,        /* the CUDA runtime refused a launch or query */
-    MOE_ERR_NONFINITE = 5,   /* device: a logit row holds NaN, or its maximum is +-inf */
+    MOE_ERR_NONFINITE = 5,   /* device: a logit row holds NaN, or its maximum is +-inf; a norm of
+                                gradients is infinite or NaN */
     MOE_ERR_BAD_EXPERT = 6,  /* device: an expert id outside [0,E) or repeated within a token */
     MOE_ERR_TIMEOUT = 7,     /* device: a pipeline wait gave up (the kernel returned, no hang) */
     MOE_ERR_CHECK = 8        /* device: a dispatch consistency check failed (MOE_FLAG_DEBUG_CHECKS,
-                                moe_check_dispatch) */
+                                moe_check_dispatch); offsets or slots out of range (moe_linear_*,
+                                moe_combine_rows*) */
 };
 
 /* Flags (moe_shape_t.flags). */
@@ -530,7 +532,7 @@ enum {
  * and rows outside every group are neither read into a result nor written.
  * expert_offsets = NULL is the dense product: E = 1 and all rows. Offsets that
  * break the rule set MOE_ERR_CHECK in *status, and the call treats every
- * group as empty. */
+ * group as empty. With rows = 0 they are not read. */
 typedef struct moe_linear {
     int32_t rows, d_in, d_out;
     int32_t E;
@@ -607,7 +609,8 @@ enum {
     MOE_TYPE_BF16 = 1
 };
 
-/* Workspace of the two calls below, for any tensors. */
+/* Workspace of the two calls below, for any tensors. Calls that share one must be
+ * ordered on the GPU, replays of captured graphs among them. */
 #define MOE_GRAD_WS_BYTES 65536
 
 /* norm[0] = sqrt(sum over all tensors of sum g^2), fp32, on the device.
@@ -631,6 +634,7 @@ MOE_API int moe_grad_norm(int n, const void *const *grads, const int64_t *numel,
  *   outs   HOST array of n device pointers of the same types, or NULL: in
  *          place. outs[i] may be grads[i]; no other overlap between any two of
  *          the tensors.
+ * c is an fp32 number: below 2^-126 (a norm past 8e37 max_norm) it has fewer bits.
  * In place, a factor of 1 writes nothing. A norm that is infinite or NaN sets
  * MOE_ERR_NONFINITE; the gradients are then left as they are (out of place:
  * copied), so that the caller can skip the step. max_norm must be > 0 and not

@@ -27,7 +27,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxTensors = 96;       // tensors of one launch (their parameters stay below 4 KB)
 constexpr int kChunkVecs = 4096;      // 64 KB of a tensor: 16 vectors a thread
 constexpr int kCtasPerSm = 8;
-constexpr int kMaxCtas = MOE_GRAD_WS_BYTES / 8 / 2;   // fp64 partials; the factor in the other half
+constexpr int kMaxCtas = MOE_GRAD_WS_BYTES / 8;       // an fp64 partial each
 
 struct TensorList {
     const void *p[kMaxTensors];

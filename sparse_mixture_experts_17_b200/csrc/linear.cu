@@ -323,10 +323,20 @@ int moe_linear_backward(const moe_linear_t *shape, const moe_bf16_t *x,
     p.E = s.E;
     p.starve = (s.flags & MOE_FLAG_TEST_TIMEOUT) != 0;
     p.status = status;
-    // dz (if any) has completed when the bias sums start, and those when dx starts, ...:
-    // each of the three lets its successor start only after its own wait, and none
-    // reads what another writes. (4096 x 2048 -> 4096: dx and dW are 128 tiles each for
-    // 74 pairs of SMs, and two rounds of one leave 20 pairs to the other.)
+    // The bias sums, dx and dW run beside each other (4096 x 2048 -> 4096: dx and dW are 128
+    // tiles each for 74 pairs of SMs, and two rounds of one leave 20 pairs to the other). That
+    // is sound because
+    //  - the first kernel after dz (the bias sums; without them dx, or dW alone, which is then
+    //    not late) lets its successor start only after its own wait: by then dz has
+    //    completed, and so has whatever ran before the call;
+    //  - a late product lets its successor start at once, waits for nothing, reads nothing
+    //    that a kernel of this call behind dz writes, and writes nothing that one reads
+    //    (dx, dW, the parts of dW and the bias sums' parts are apart);
+    //  - it waits for its predecessor before each of its ways out, so that whatever waits for
+    //    the call's last kernel has waited for all of them.
+    // A late product thus reads dz, and what came before the call, without a wait of its own:
+    // what it rests on is that their kernels had completed, their writes with them, before
+    // it was started.
     p.late = dbias != nullptr;
     if (dx) {
         p.out = dx;

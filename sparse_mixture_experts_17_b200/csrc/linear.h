@@ -26,9 +26,10 @@ struct LinArgs {
     int rows, d_in, d_out, E, act;
     int splits;                   // LIN_DW
     // The product needs nothing of the kernel launched just before it, and what it does
-    // need had completed before that one let its successor start: it starts at once,
-    // beside that kernel's last CTAs, and waits for it only before it ends (so that
-    // whatever waits for this product has waited for both).
+    // need had completed before that one was let start its successor: it starts at once,
+    // beside that kernel, and lets its own successor start at once too; it waits for its
+    // predecessor only before it ends, on every way out (so that whatever waits for this
+    // product has waited for both). See moe_linear_backward.
     bool late;
     bool starve;                  // MOE_FLAG_TEST_TIMEOUT
     uint32_t *status;

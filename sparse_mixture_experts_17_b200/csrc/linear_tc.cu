@@ -1346,6 +1346,15 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
     const int avg = ceil_div(a.rows, groups);
     const long long pair_tiles = (long long)groups * ceil_div(avg, kTileC) * ceil_div(M, 256);
     const int sms = num_sms();
+    // Pairs of SMs where each has a tile and the groups average more than 32 rows; single SMs
+    // below, where the weights' stream decides. us single / pair, k = 8 of 256 experts of 4096
+    // -> 4096: 16 tokens 515 / 576, 128 tokens 1247 / 1393, 1024 tokens (32 rows a group)
+    // 1391 / 1485, the same by a Zipf law of 1.1 (1 to 900 rows) 1533 / 1538. Above: 4096 rows
+    // in 64 groups 409 / 411, 1280 x 4096 -> 4096 52 / 47, dx of 4096 x 4096 -> 2048 56 / 49; but 128 x
+    // 4096 -> 14336 28.2 / 30.0. Below a tile each: 512 x 4096 -> 4096 21 / 27, 4096 x 2048 -> 1024
+    // 14.4 / 17.1. The average does not show how the rows fall, and the sizes are on the
+    // device: 8192 rows are 420 / 240 when they all are one of 256 groups, 1683 / 1637 when the
+    // other 255 have one row each.
     if (pair_tiles >= sms / 2 && avg > 32) {
         // Double tiles share the weights' part of a stage between 512 rows: a quarter less
         // from L2 for the same products, at the price of an epilogue that overlaps less.
@@ -1388,6 +1397,18 @@ int launch_rows(const LinArgs &a, cudaStream_t st)
 
 } // namespace
 
+// As many as there are SMs for the tiles, at most 16, none shorter than 512 rows: the sums over
+// the rows are one chain of blocks a tile, and few tiles leave most SMs idle. us with 1 / 2 / 4 /
+// 8 parts (the rule's own number, where it is another), dense layers:
+//   512 -> 512 (4 tiles), 4096 rows 29.5 / 19.9 / 13.3 / 11.1; 16384 rows 94 / 50 / 29 / 19 (16: 22)
+//   1024 -> 1024 (16 tiles), 1024 rows 11.2 / 11.1 (2); 4096 rows 29.5 / 20.8 / 15.4 / 18.2 (8: 22.0);
+//     16384 rows 97 / 53 / 36 / 45 (9: 44)
+//   1536 -> 1536 (36 tiles), 4096 rows 28.0 / 22.0 / 24.9 / 36.1 (4); 16384 rows 102 / 77 / 72 / 92 (4)
+//   2048 -> 2048 (64 tiles), 1024 rows 12.3 / 19.2 (2); 4096 rows 31.4 / 41.9 (2: 36.1); 16384 rows
+//     126 / 138 (2: 141)
+//   2304 -> 2304 (81 tiles, never split), 4096 rows 50.8 / 50.0; 16384 rows 200 / 193
+// The tiles run on pairs of SMs, so from 38 tiles on, and for short sums below that, the
+// rule takes more parts than pay.
 int lin_dw_splits(const moe_linear_t &s)
 {
     const long long tiles = (long long)s.E * ceil_div(s.d_in, 256) * ceil_div(s.d_out, kTileC);
