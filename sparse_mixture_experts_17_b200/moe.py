@@ -542,8 +542,8 @@ def _address(a):
 
 def alloc_grad_workspace(grads=(), device="cuda") -> torch.Tensor:
     """A workspace for moe_grad_norm and moe_clip_grads, on the gradients' device."""
-    dev = grads[0].device if len(grads) else device
-    return torch.empty(MOE_GRAD_WS_BYTES, dtype=torch.uint8, device=dev)
+    first = next(iter(grads), None)
+    return torch.empty(MOE_GRAD_WS_BYTES, dtype=torch.uint8, device=device if first is None else first.device)
 
 
 _GRADS = (("norm", "status", "ws", "grads", "outs"), (F32, U32, None, None, None), (1, 1, None, None, None))
